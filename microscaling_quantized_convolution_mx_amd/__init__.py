@@ -292,3 +292,11 @@ def mx_im2col_cbf(d: mx_conv_desc, x, xcol, stream=None) -> None:
 def mx_dequantize(d: mx_conv_desc, role: int, q, dst, stream=None) -> None:
     args = (ctypes.byref(d), role, _q(q, d, role, "q"), _buf(dst, 4 * role_numel(d, role), "dst"))
     _check(lib().mx_dequantize(*args, _stream(stream)), "mx_dequantize")
+
+
+# The microscaled linear layers and the gradient clip (include/mxlinear.h).
+from .linear import (  # noqa: E402
+    MX_BF16, MX_F16, MX_F32, MX_FORM_COLS, MX_FORM_ROWS, LINEAR_EXPORTS, LINEAR_MAX_EXPERTS, GradList, LinearQTensor,
+    linear_desc, mx_grad_clip, mx_grad_list, mx_grad_norm, mx_grad_workspace_bytes, mx_linear_apply,
+    mx_linear_code_bytes, mx_linear_dequantize, mx_linear_desc, mx_linear_dgrad, mx_linear_fwd, mx_linear_qtensor,
+    mx_linear_quantize, mx_linear_scale_bytes, mx_linear_wgrad, mx_linear_workspace_bytes)

@@ -1,0 +1,207 @@
+// Global norm over many gradients and clipping by it (mxlinear.h).
+//
+// Two launches for up to kTensors tensors (each further kTensors add two):
+//   k_grad_sum   reads every gradient once; a workgroup sums the squares of
+//                its chunks and leaves one fp64 partial
+//   k_grad_clip  every workgroup adds all partials in the same order (a few
+//                KiB from L2), so all of them hold the same norm without a
+//                launch between, then scales its chunks
+// Bound by memory: two reads and one write.  Sums are fp64: the squares of
+// any finite fp32 fit, and the adds are far below the vector units' rate.
+//
+// The tensors' addresses and sizes travel in the kernel's arguments, so no
+// table has to be copied to the device.  Work is dealt in chunks of kChunk
+// elements over all tensors; a workgroup takes every gridDim.x-th chunk.
+#include "linear.h"
+
+namespace mx {
+namespace {
+
+constexpr int kTensors = 96;       // per launch: the arguments stay below 4 KiB
+constexpr int kThreads = 256;
+constexpr int kChunk = 8192;       // elements
+constexpr int kMaxGroups = 1024;   // workgroups, and partials, per launch
+
+struct Batch {
+  const void* grad[kTensors];
+  void* out[kTensors];
+  int64_t numel[kTensors];
+  int32_t first[kTensors + 1];  // first chunk of each tensor
+  uint8_t dtype[kTensors];
+  int32_t count;
+};
+
+template <class T> struct Pack { static constexpr int N = 16 / sizeof(T); };
+
+template <class T>
+__device__ __forceinline__ void unpack(uint4 v, float* x) {
+  const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+  for (int i = 0; i < Pack<T>::N; ++i) x[i] = to_f32(e[i]);
+}
+
+// the tensor of chunk c
+__device__ __forceinline__ int tensor_of(const Batch& b, int c) {
+  int lo = 0, hi = b.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (b.first[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <class T>
+__device__ __forceinline__ double sum_chunk(const T* __restrict__ g, int64_t n) {
+  constexpr int N = Pack<T>::N;
+  double s = 0.0;
+  if (reinterpret_cast<uintptr_t>(g) % 16 == 0) {
+    const int64_t packs = n / N;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
+      float x[N];
+      unpack<T>(reinterpret_cast<const uint4*>(g)[i], x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), s);
+    }
+    const int64_t i = packs * N + threadIdx.x;
+    if (i < n) {
+      const double x = to_f32(g[i]);
+      s = __builtin_fma(x, x, s);
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+      const double x = to_f32(g[i]);
+      s = __builtin_fma(x, x, s);
+    }
+  }
+  return s;
+}
+
+template <class T>
+__device__ __forceinline__ void scale_chunk(const T* g, T* o, int64_t n, float f) {
+  constexpr int N = Pack<T>::N;
+  int64_t done = 0;
+  if (reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+    const int64_t packs = n / N;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
+      float x[N];
+      unpack<T>(reinterpret_cast<const uint4*>(g)[i], x);
+      uint4 w;
+      T* e = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int j = 0; j < N; ++j) e[j] = from_f32<T>(x[j] * f);
+      reinterpret_cast<uint4*>(o)[i] = w;
+    }
+    done = packs * N;
+  }
+  for (int64_t i = done + threadIdx.x; i < n; i += kThreads) o[i] = from_f32<T>(to_f32(g[i]) * f);
+}
+
+// Sum over the workgroup, the same in every thread, in a fixed order.
+__device__ __forceinline__ double group_sum(double s) {
+  __shared__ double part[kThreads / 64];
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) s += __shfl_xor(s, d);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) s += part[i];
+  __syncthreads();
+  return s;
+}
+
+__global__ __launch_bounds__(kThreads) void k_grad_sum(const Batch b, double* __restrict__ partial) {
+  double s = 0.0;
+  for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
+    const int t = tensor_of(b, c);
+    const int64_t at = static_cast<int64_t>(c - b.first[t]) * kChunk;
+    const int64_t n = min(static_cast<int64_t>(kChunk), b.numel[t] - at);
+    if (b.dtype[t] == MX_BF16) s += sum_chunk(static_cast<const bf16_t*>(b.grad[t]) + at, n);
+    else if (b.dtype[t] == MX_F16) s += sum_chunk(static_cast<const f16_t*>(b.grad[t]) + at, n);
+    else s += sum_chunk(static_cast<const float*>(b.grad[t]) + at, n);
+  }
+  s = group_sum(s);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// write: this launch's first workgroup stores the norm
+__global__ __launch_bounds__(kThreads) void k_grad_clip(const Batch b, const double* __restrict__ partial, int partials,
+                                                         float max_norm, float* __restrict__ norm, int write) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < partials; i += kThreads) s += partial[i];
+  s = group_sum(s);
+  const float nrm = static_cast<float>(__builtin_sqrt(s));
+  if (write && blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
+  if (b.count == 0) return;
+  const float q = max_norm / (nrm + 1e-6f);
+  const float f = q < 1.0f || q != q ? q : 1.0f;
+  for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
+    const int t = tensor_of(b, c);
+    if (f == 1.0f && b.grad[t] == b.out[t]) continue;
+    const int64_t at = static_cast<int64_t>(c - b.first[t]) * kChunk;
+    const int64_t n = min(static_cast<int64_t>(kChunk), b.numel[t] - at);
+    if (b.dtype[t] == MX_BF16) scale_chunk(static_cast<const bf16_t*>(b.grad[t]) + at, static_cast<bf16_t*>(b.out[t]) + at, n, f);
+    else if (b.dtype[t] == MX_F16) scale_chunk(static_cast<const f16_t*>(b.grad[t]) + at, static_cast<f16_t*>(b.out[t]) + at, n, f);
+    else scale_chunk(static_cast<const float*>(b.grad[t]) + at, static_cast<float*>(b.out[t]) + at, n, f);
+  }
+}
+
+// The next batch of non-empty tensors from i on.  The caller has checked that
+// all chunks together fit an int32.
+void fill(const mx_grad_list* l, int& i, Batch& b) {
+  b.count = 0;
+  int64_t chunks = 0;
+  for (; i < l->count && b.count < kTensors; ++i) {
+    if (l->numel[i] <= 0) continue;
+    const int64_t more = (l->numel[i] + kChunk - 1) / kChunk;
+    b.grad[b.count] = l->grads[i];
+    b.out[b.count] = l->out ? l->out[i] : nullptr;
+    b.numel[b.count] = l->numel[i];
+    b.dtype[b.count] = static_cast<uint8_t>(l->dtypes[i]);
+    b.first[b.count] = static_cast<int32_t>(chunks);
+    chunks += more;
+    b.first[++b.count] = static_cast<int32_t>(chunks);
+  }
+}
+
+unsigned groups(const Batch& b) {
+  const int c = b.first[b.count];
+  return static_cast<unsigned>(c < kMaxGroups ? c : kMaxGroups);
+}
+
+}  // namespace
+
+size_t grad_workspace_bytes(int32_t count) {
+  return static_cast<size_t>((count + kTensors - 1) / kTensors) * kMaxGroups * sizeof(double);
+}
+
+hipError_t launch_grad_clip(const mx_grad_list* l, bool clip, float max_norm, float* norm, void* workspace, hipStream_t s) {
+  double* partial = static_cast<double*>(workspace);
+  int partials = 0;
+  static_assert(sizeof(Batch) + 64 <= 4096);
+  Batch b;
+  for (int i = 0; i < l->count;) {
+    fill(l, i, b);
+    if (b.count == 0) break;
+    const unsigned wgs = groups(b);
+    hipLaunchKernelGGL(k_grad_sum, dim3(wgs), dim3(kThreads), 0, s, b, partial + partials);
+    partials += static_cast<int>(wgs);
+  }
+  bool first = true;
+  for (int i = 0; clip && i < l->count;) {
+    fill(l, i, b);
+    if (b.count == 0) break;
+    hipLaunchKernelGGL(k_grad_clip, dim3(groups(b)), dim3(kThreads), 0, s, b, partial, partials, max_norm, norm, first ? 1 : 0);
+    first = false;
+  }
+  if (first) {
+    b.count = 0;
+    hipLaunchKernelGGL(k_grad_clip, dim3(1), dim3(kThreads), 0, s, b, partial, partials, max_norm, norm, 1);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -1,0 +1,427 @@
+// The products of the microscaled linear layers on the scaled FP4 MFMA.
+//
+// out[i][j] = sum_c a[i][c] b[j][c] with both operands in a form whose
+// columns are c (mxlinear.h):
+//   fwd    a = X rows,   b = W rows,   c = in features
+//   dgrad  a = dY rows,  b = W cols,   c = out features
+//   wgrad  a = dY cols,  b = X cols,   c = tokens
+// so one kernel serves all three.  With experts, fwd and dgrad take the rows
+// of `a` in segments with a weight matrix each (ROWS), wgrad the columns in
+// segments with an output matrix each (CONTRACT).
+#include "linear.h"
+
+#include <type_traits>
+#include <utility>
+
+namespace mx {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+template <int I>
+struct Idx {
+  static constexpr int value = I;
+};
+template <int N, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  [&]<int... I>(std::integer_sequence<int, I...>) { (f(Idx<I>{}), ...); }(std::make_integer_sequence<int, N>());
+}
+
+struct ProductParams {
+  const uint8_t *a, *as, *b, *bs;  // codes and scales
+  void* out;
+  float* partial;          // split products: fp32 [splits][rows][cols] sums, else null
+  int64_t akt, bkt;        // column tiles of a stripe
+  int64_t bmat;            // ROWS: padded rows of one weight matrix in b
+  int64_t a_rows, b_rows;  // padded rows of a and b (of all matrices)
+  int64_t rows, cols;      // of out (ROWS: rows = tokens; CONTRACT: of one expert's matrix)
+  int64_t ld;
+  int ktiles;              // ROWS and one layer: column tiles to contract
+  int tokens;
+  const int32_t* offsets;
+  int experts;
+  int tiles_i, tiles_j;    // output tiles (ROWS with experts: tiles_i is an upper bound over all of them)
+  int splits, split_steps; // pieces of the contraction and steps of each
+};
+
+__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+
+// TILE x TILE outputs per workgroup, 4 waves of TILE/2 x TILE/2 in MFMAs of
+// 32x32x64.
+//
+// One step contracts 128 columns: two MFMA slices.  Each thread copies
+// 16-byte pieces of the operands' tiles from memory into one of three LDS
+// stages, in the order they are stored: the pieces are fetched into registers
+// two steps before they are written to LDS, which happens two steps before
+// they are read.  A tile in LDS is read as it is, 64 lanes x 16 consecutive
+// bytes, which is free of bank conflicts.
+template <class T, int TILE, bool CONTRACT>
+__global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
+  constexpr int RM = TILE / 64;               // MFMA rows and columns of a wave
+  constexpr int NQ = TILE / 64;               // 16-byte pieces a thread copies per operand and step
+  constexpr int kOpnd = (TILE / 32) * kStepTiles * kTileBytes;
+  constexpr int kOpndS = (TILE / 128) * kStepTiles * kScaleBytes;
+  constexpr int kStage = 2 * kOpnd + 2 * kOpndS;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage];
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+
+  // Work: (expert, row tile, column tile, split).  Blocks go to the 8 XCDs in
+  // turn; XCD x takes the x-th eighth of the work, so that what its blocks
+  // share stays in its L2.
+  int ti, tj, sp = 0;
+  int64_t arow = 0, brow = 0;      // first padded rows of the tile in a and b
+  int64_t orow = 0, rleft, cleft;  // first output row, rows and columns left of the matrix from the tile on
+  int64_t k0 = 0;                  // first column tile
+  int ksteps;                      // steps of the whole contraction
+  T* out = static_cast<T*>(p.out);
+  {
+    int64_t total;
+    if (CONTRACT || p.experts == 0) total = static_cast<int64_t>(p.tiles_i) * p.tiles_j * (CONTRACT && p.experts > 0 ? p.experts : p.splits);
+    else {
+      Segment s;
+      int ti_all = 0;
+      find_segment(p.offsets, p.experts, p.tokens, -1, TILE, s, &ti_all);
+      total = static_cast<int64_t>(ti_all) * p.tiles_j;
+    }
+    const int64_t per = (total + 7) / 8;
+    const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
+    int64_t w = x * per + i;
+    if (i >= per || w >= total) return;
+    // groups of 4 row tiles, walked column by column
+    const int64_t plane = static_cast<int64_t>(p.tiles_i) * p.tiles_j;
+    int rows_t = p.tiles_i;
+    int z = 0;
+    if (CONTRACT || p.experts == 0) {
+      z = static_cast<int>(w / plane);
+      w -= z * plane;
+    } else {
+      rows_t = static_cast<int>(total / p.tiles_j);
+    }
+    constexpr int G = 4;
+    const int64_t band = static_cast<int64_t>(G) * p.tiles_j;
+    const int bi = static_cast<int>(w / band);
+    const int r = static_cast<int>(w - bi * band);
+    const int h = min(G, rows_t - bi * G);
+    ti = bi * G + r % h;
+    tj = r / h;
+    if constexpr (CONTRACT) {
+      arow = static_cast<int64_t>(ti) * TILE;
+      orow = arow;
+      rleft = p.rows - orow;
+      if (p.experts > 0) {
+        Segment s;
+        find_segment(p.offsets, p.experts, p.tokens, z, 0, s);
+        k0 = s.prow / kTileC;
+        ksteps = (s.len + kPad - 1) / kPad;
+        out += static_cast<int64_t>(z) * p.rows * p.ld;
+      } else {
+        ksteps = p.ktiles / kStepTiles;
+        sp = z;
+      }
+      brow = static_cast<int64_t>(tj) * TILE;
+    } else {
+      ksteps = p.ktiles / kStepTiles;
+      if (p.experts > 0) {
+        Segment s;
+        find_segment(p.offsets, p.experts, p.tokens, ti, TILE, s);
+        arow = s.prow + static_cast<int64_t>(s.unit) * TILE;
+        orow = s.row0 + static_cast<int64_t>(s.unit) * TILE;
+        rleft = s.len - static_cast<int64_t>(s.unit) * TILE;
+        brow = s.e * p.bmat;
+      } else {
+        sp = z;
+        arow = orow = static_cast<int64_t>(ti) * TILE;
+        rleft = p.rows - orow;
+      }
+      brow += static_cast<int64_t>(tj) * TILE;
+    }
+    cleft = p.cols - static_cast<int64_t>(tj) * TILE;
+  }
+  int s_begin = 0, nsteps = ksteps;
+  if (p.partial) {
+    s_begin = min(ksteps, sp * p.split_steps);
+    nsteps = min(ksteps, s_begin + p.split_steps) - s_begin;
+  }
+  k0 += static_cast<int64_t>(s_begin) * kStepTiles;
+
+  // Copy: wave w's piece q is tile w%2 of stripe 2q + w/2.  A stripe past the
+  // operand's end is read as its last one: those outputs are not stored.
+  const uint8_t* asrc[NQ];
+  const uint8_t* bsrc[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int64_t st = 2 * q + (wave >> 1);
+    const int64_t sa = min(arow / kTileR + st, p.a_rows / kTileR - 1), sb = min(brow / kTileR + st, p.b_rows / kTileR - 1);
+    asrc[q] = p.a + (sa * p.akt + k0 + (wave & 1)) * kTileBytes;
+    bsrc[q] = p.b + (sb * p.bkt + k0 + (wave & 1)) * kTileBytes;
+  }
+  // scales: dword t of a step is lane t%64 of tile (t/64)%2 of the 128 rows t/128
+  const bool scaler = TILE == 256 || tid < 128;
+  const int64_t ga = min(arow / kPad + (wave >> 1), p.a_rows / kPad - 1), gb = min(brow / kPad + (wave >> 1), p.b_rows / kPad - 1);
+  const uint8_t* assrc = p.as + (ga * p.akt + k0 + (wave & 1)) * kScaleBytes;
+  const uint8_t* bssrc = p.bs + (gb * p.bkt + k0 + (wave & 1)) * kScaleBytes;
+
+  struct Raw {
+    i32x4 a[NQ], b[NQ];
+    int sa, sb;
+  };
+  Raw r0, r1;
+  // a step past the last one reads the last one again
+  auto fetch_one = [&](Raw& raw, int step, int q) {
+    const int64_t o = static_cast<int64_t>(min(step, nsteps - 1)) * (kStepTiles * kTileBytes);
+    raw.a[q] = reinterpret_cast<const i32x4*>(asrc[q] + o)[lane];
+    raw.b[q] = reinterpret_cast<const i32x4*>(bsrc[q] + o)[lane];
+  };
+  auto fetch_scales = [&](Raw& raw, int step) {
+    const int64_t o = static_cast<int64_t>(min(step, nsteps - 1)) * (kStepTiles * kScaleBytes);
+    raw.sa = reinterpret_cast<const int*>(assrc + o)[lane];
+    raw.sb = reinterpret_cast<const int*>(bssrc + o)[lane];
+  };
+  auto fetch = [&](Raw& raw, int step) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) fetch_one(raw, step, q);
+    fetch_scales(raw, step);
+  };
+  // ... and is written with zeros for a's codes.  (A scale that is NaN has
+  // already made those sums NaN.)
+  auto stage_write = [&](const Raw& raw, uint8_t* st, int step) {
+    const int m = step < nsteps ? -1 : 0;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      reinterpret_cast<i32x4*>(st)[q * 256 + tid] = raw.a[q] & m;
+      reinterpret_cast<i32x4*>(st + kOpnd)[q * 256 + tid] = raw.b[q];
+    }
+    if (scaler) {
+      reinterpret_cast<int*>(st + 2 * kOpnd)[tid] = raw.sa;
+      reinterpret_cast<int*>(st + 2 * kOpnd + kOpndS)[tid] = raw.sb;
+    }
+  };
+
+  f32x16 acc[RM][RM];
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  struct Frags {
+    i32x8 a[RM], b[RM];
+    int sa, sb;
+  };
+  Frags fA, fB;
+  auto read_frags = [&](const uint8_t* st, int j, Frags& f) {
+    // a wave of 64 rows uses two bytes of its 128 rows' scales
+    const uint8_t* s = st + 2 * kOpnd;
+    if constexpr (RM == 4) {
+      f.sa = reinterpret_cast<const int*>(s + (wm * kStepTiles + j) * kScaleBytes)[lane];
+      f.sb = reinterpret_cast<const int*>(s + kOpndS + (wn * kStepTiles + j) * kScaleBytes)[lane];
+    } else {
+      f.sa = reinterpret_cast<const uint16_t*>(s + j * kScaleBytes)[2 * lane + wm];
+      f.sb = reinterpret_cast<const uint16_t*>(s + kOpndS + j * kScaleBytes)[2 * lane + wn];
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      f.a[i] = operand(reinterpret_cast<const i32x4*>(st + ((wm * RM + i) * kStepTiles + j) * kTileBytes)[lane]);
+      f.b[i] = operand(reinterpret_cast<const i32x4*>(st + kOpnd + ((wn * RM + i) * kStepTiles + j) * kTileBytes)[lane]);
+    }
+  };
+
+  // Step s, on stage s%3, with slice 0's operands read during step s-1: write
+  // step s+2 (fetched two steps ago) into stage (s+2)%3, whose last reads
+  // were in step s-1; read slice 1; multiply slice 0, fetching step s+4
+  // between the MFMAs; read slice 0 of step s+1, complete since the barrier
+  // of step s-1; multiply slice 1; barrier.  Steps run in pairs so that the
+  // two register sets alternate statically; the extra step of an odd count
+  // multiplies zeros.
+  auto slice = [&](const Frags& f, Raw& raw, int fs, bool first) {
+    static_for<RM>([&](auto ic) {
+      constexpr int I = decltype(ic)::value;
+      static_for<RM>([&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[I], f.b[J], acc[I][J], 4, 4, I, f.sa, J, f.sb);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (J == 0) {
+          if (first) fetch_one(raw, fs, I);
+          else if (I == 0) fetch_scales(raw, fs);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+    });
+  };
+  auto step = [&](int s, const uint8_t* cur, const uint8_t* next, uint8_t* to, Raw& raw) {
+    stage_write(raw, to, s + 2);
+    read_frags(cur, 1, fB);
+    __builtin_amdgcn_sched_barrier(0);
+    slice(fA, raw, s + 4, true);
+    read_frags(next, 0, fA);
+    __builtin_amdgcn_sched_barrier(0);
+    slice(fB, raw, s + 4, false);
+    // keeps the MFMAs ahead of the barrier
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < RM; ++j) asm volatile("" : "+a"(acc[i][j]));
+    __syncthreads();
+  };
+  if (nsteps > 0) {
+    fetch(r0, 0);
+    fetch(r1, 1);
+    stage_write(r0, lds, 0);
+    stage_write(r1, lds + kStage, 1);
+    fetch(r0, 2);
+    fetch(r1, 3);
+    __syncthreads();
+    read_frags(lds, 0, fA);
+    int c = 0;
+    for (int s = 0; s < nsteps; s += 2) {
+      const int c1 = c == 2 ? 0 : c + 1, c2 = c1 == 2 ? 0 : c1 + 1;
+      step(s, lds + c * kStage, lds + c1 * kStage, lds + c2 * kStage, r0);
+      step(s + 1, lds + c1 * kStage, lds + c2 * kStage, lds + c * kStage, r1);
+      c = c2;
+    }
+  }
+
+  // lane l holds column l%32 and rows 8(v/4) + 4(l/32) + v%4 of a 32x32
+  const int64_t tr = wm * (TILE / 2) + 4 * (lane >> 5), tc = wn * (TILE / 2) + (lane & 31);
+  if (p.partial) {
+    float* d = p.partial + (static_cast<int64_t>(sp) * p.rows + orow) * p.cols + static_cast<int64_t>(tj) * TILE;
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+      for (int j = 0; j < RM; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int64_t r = tr + 32 * i + 8 * (v / 4) + v % 4, c = tc + 32 * j;
+          if (r < rleft && c < cleft) d[r * p.cols + c] = acc[i][j][v];
+        }
+    return;
+  }
+  T* d = out + orow * p.ld + static_cast<int64_t>(tj) * TILE;
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RM; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t r = tr + 32 * i + 8 * (v / 4) + v % 4, c = tc + 32 * j;
+        if (r < rleft && c < cleft) d[r * p.ld + c] = from_f32<T>(acc[i][j][v]);
+      }
+}
+
+// Sums the pieces of a split product in their order.
+template <class T>
+__global__ __launch_bounds__(256) void k_lin_reduce(const float* __restrict__ partial, int splits, int64_t rows, int64_t cols,
+                                                     T* __restrict__ out, int64_t ld) {
+  const int64_t n = rows * cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    float s = partial[i];
+    for (int q = 1; q < splits; ++q) s += partial[q * n + i];
+    const int64_t r = i / cols;
+    out[r * ld + (i - r * cols)] = from_f32<T>(s);
+  }
+}
+
+struct Plan {
+  int tile;     // 128 or 256
+  int64_t tiles_i, tiles_j;
+  int splits, split_steps;
+  int64_t units;  // workgroups, at most
+};
+
+Plan make_plan(const LinGeom& g, LinOp op) {
+  Plan pl{};
+  const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
+  const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
+  const int64_t used = g.m < g.ew ? g.m : g.ew;
+  auto count = [&](int tile) {
+    const int64_t extra = op != LIN_WGRAD && g.e > 0 ? used : 0;
+    pl.tile = tile;
+    pl.tiles_i = (rows + tile - 1) / tile + extra;
+    pl.tiles_j = (cols + tile - 1) / tile;
+    pl.units = pl.tiles_i * pl.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
+  };
+  count(256);
+  if (pl.units < 256) count(128);
+  pl.splits = 1;
+  pl.split_steps = static_cast<int>(contract / kPad);
+  if (g.e == 0 && pl.units > 0 && pl.units <= 128) {
+    // enough pieces to give every CU a workgroup, of 4 steps at least
+    const int64_t steps = contract / kPad;
+    int64_t s = 256 / pl.units;
+    if (s > steps / 4) s = steps / 4;
+    if (s > 1) {
+      pl.split_steps = static_cast<int>((steps + s - 1) / s);
+      pl.splits = static_cast<int>((steps + pl.split_steps - 1) / pl.split_steps);
+    }
+  }
+  return pl;
+}
+
+}  // namespace
+
+size_t lin_product_workspace(const LinGeom& g, LinOp op) {
+  if (g.m == 0) return 0;
+  const Plan pl = make_plan(g, op);
+  if (pl.splits <= 1) return 0;
+  const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
+  return static_cast<size_t>(pl.splits * rows * cols) * sizeof(float);
+}
+
+hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
+                              void* out, mx_dtype dtype, int64_t ld, const int32_t* offsets, void* workspace,
+                              hipStream_t s) {
+  const Plan pl = make_plan(g, op);
+  if (pl.units == 0) return hipSuccess;
+  ProductParams p{};
+  const mx_role ra = op == LIN_FWD ? MX_ROLE_ACT : MX_ROLE_GRAD, rb = op == LIN_WGRAD ? MX_ROLE_ACT : MX_ROLE_WEIGHT;
+  const mx_form fa = op == LIN_WGRAD ? MX_FORM_COLS : MX_FORM_ROWS, fb = op == LIN_FWD ? MX_FORM_ROWS : MX_FORM_COLS;
+  p.a = static_cast<const uint8_t*>(fa == MX_FORM_ROWS ? aq->rows : aq->cols);
+  p.as = fa == MX_FORM_ROWS ? aq->row_scales : aq->col_scales;
+  p.b = static_cast<const uint8_t*>(fb == MX_FORM_ROWS ? bq->rows : bq->cols);
+  p.bs = fb == MX_FORM_ROWS ? bq->row_scales : bq->col_scales;
+  int64_t c;
+  form_dims(g, ra, fa, p.a_rows, c);
+  p.akt = c / kTileC;
+  p.ktiles = static_cast<int>(c / kTileC);
+  form_dims(g, rb, fb, p.bmat, c);
+  p.bkt = c / kTileC;
+  p.b_rows = p.bmat * form_matrices(g, rb);
+  p.rows = op == LIN_WGRAD ? g.n : g.m;
+  p.cols = op == LIN_FWD ? g.n : g.k;
+  p.out = out;
+  p.ld = ld;
+  p.tokens = static_cast<int>(g.m);
+  p.offsets = offsets;
+  p.experts = g.e;
+  p.tiles_i = static_cast<int>(pl.tiles_i);
+  p.tiles_j = static_cast<int>(pl.tiles_j);
+  p.splits = pl.splits;
+  p.split_steps = pl.split_steps;
+  p.partial = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  const unsigned grid = static_cast<unsigned>((pl.units * pl.splits + 7) / 8 * 8);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, s, p); };
+    if (op == LIN_WGRAD) pl.tile == 256 ? launch(k_lin_product<T, 256, true>) : launch(k_lin_product<T, 128, true>);
+    else pl.tile == 256 ? launch(k_lin_product<T, 256, false>) : launch(k_lin_product<T, 128, false>);
+    if (pl.splits > 1) {
+      const int64_t n = p.rows * p.cols;
+      const unsigned wgs = static_cast<unsigned>(n / 256 < 2048 ? (n + 255) / 256 : 2048);
+      hipLaunchKernelGGL(k_lin_reduce<T>, dim3(wgs), dim3(256), 0, s, p.partial, p.splits, p.rows, p.cols, static_cast<T*>(out), ld);
+    }
+  };
+  switch (dtype) {
+    case MX_BF16: go(bf16_t{}); break;
+    case MX_F16: go(f16_t{}); break;
+    default: go(float{}); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -1,0 +1,136 @@
+"""Global gradient norm and clipping against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import microscaling_quantized_convolution_mx_amd as mx
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+# half a step of the type at a value, relative
+UNIT = {F32: 2.0 ** -24, BF16: 2.0 ** -8, F16: 2.0 ** -11}
+
+
+def tensors(sizes, dts, seed=1, scale=1.0):
+    g = np.random.default_rng(seed)
+    return [torch.from_numpy((g.standard_normal(n) * scale).astype(np.float32)).to(dts[i % len(dts)]).to(DEV)
+            for i, n in enumerate(sizes)]
+
+
+def clip(grads, max_norm, out=None):
+    lst = mx.GradList(grads, out)
+    norm = torch.full((1,), -1.0, device=DEV)
+    ws = torch.full((max(mx.mx_grad_workspace_bytes(lst), 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    mx.mx_grad_clip(lst, max_norm, norm, ws)
+    torch.cuda.synchronize()
+    return float(norm)
+
+
+def norm64(grads):
+    return math.sqrt(sum(float((g.double().cpu() ** 2).sum()) for g in grads))
+
+
+def check(grads, max_norm):
+    want = norm64(grads)
+    outs = [torch.full_like(g, 5.0) for g in grads]
+    got = clip(grads, max_norm, outs)
+    # one rounding to fp32; the fp64 sums' own error is far below it
+    assert abs(got - want) <= 2.0 ** -23 * want
+    f = min(1.0, max_norm / (want + 1e-6)) if want else 1.0
+    for g, o in zip(grads, outs):
+        ref = g.double().cpu() * f
+        # the factor: norm, sum and quotient rounded to fp32; the product, then the type (f16: its smallest step too)
+        lim = ref.abs() * (5 * 2.0 ** -24 + UNIT[g.dtype] * 1.01) + (2.0 ** -25 if g.dtype == F16 else 2.0 ** -134)
+        assert bool(((o.double().cpu() - ref).abs() <= lim).all())
+        if f == 1.0:
+            assert torch.equal(o, g)
+    copies = [g.clone() for g in grads]
+    assert clip(copies, max_norm) == got
+    for c, o in zip(copies, outs):
+        assert torch.equal(c, o)
+
+
+@pytest.mark.parametrize("dts", [[F32], [BF16], [F16], [F32, BF16, F16]])
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [7, 8, 9, 255, 256, 257], [8191, 8192, 8193], [100003, 5, 70000],
+                                   list(range(0, 130)), [1000] * 200])
+def test_clip(sizes, dts):
+    say("clip", sizes[:6], len(sizes), dts)
+    g = tensors(sizes, dts)
+    n = norm64(g)
+    check(g, 0.3 * n + 1e-3)
+    check(g, 2 * n + 1.0)
+
+
+def test_large():
+    g = tensors([9_000_001, 20_000_003, 17], [F32, BF16], scale=1e-3)
+    check(g, 0.1)
+
+
+def test_unaligned_parts_of_a_bucket():
+    """Gradients that are parts of one buffer start at any element."""
+    for dt in (F32, BF16, F16):
+        flat = tensors([50_000], [dt])[0]
+        parts = list(flat.split([1, 3, 4097, 8192, 20_000, 50_000 - 32_293]))
+        check(parts, 1.0)
+        out = torch.zeros_like(flat)
+        clip(parts, 1.0, list(out.split([p.numel() for p in parts])))
+        want = [p.clone() for p in parts]
+        clip(want, 1.0)
+        assert torch.equal(out, torch.cat(want))
+        # outputs that are aligned otherwise than their gradients
+        shifted = torch.zeros(flat.numel() + 1, dtype=dt, device=DEV)[1:]
+        clip([flat], 1.0, [shifted])
+        copy = flat.clone()
+        clip([copy], 1.0)
+        assert torch.equal(shifted, copy)
+
+
+def test_norm_alone():
+    g = tensors([1000, 70_001, 0, 3], [F32, BF16])
+    lst = mx.GradList(g)
+    norm = torch.zeros(1, device=DEV)
+    ws = torch.empty(mx.mx_grad_workspace_bytes(lst), dtype=torch.uint8, device=DEV)
+    mx.mx_grad_norm(lst, norm, ws)
+    assert abs(float(norm) - norm64(g)) <= 2.0 ** -23 * norm64(g)
+    norm.fill_(-1.0)
+    mx.mx_grad_norm(mx.GradList([]), norm)
+    assert float(norm) == 0.0
+    norm.fill_(-1.0)
+    mx.mx_grad_clip(mx.GradList([torch.zeros(0, device=DEV)]), 1.0, norm, ws)
+    assert float(norm) == 0.0
+
+
+def test_extreme_values():
+    # squares past the range of fp32, and below it
+    check(tensors([5000, 33], [F32], scale=1e30), 1.0)
+    check(tensors([5000, 33], [F32], scale=1e-30), 1e-32)
+    # zero gradients, and a largest norm of zero
+    z = [torch.zeros(100, device=DEV)]
+    assert clip(z, 1.0) == 0.0 and not bool(z[0].any())
+    g = tensors([1000], [F32])
+    clip(g, 0.0)
+    assert not bool(g[0].any())
+
+
+def test_non_finite():
+    """As the formula has it: Inf makes the factor 0 (and 0 * Inf is NaN), a NaN makes everything NaN."""
+    g = tensors([1000, 50], [F32])
+    g[1][7] = float("inf")
+    assert clip(g, 1.0) == math.inf
+    assert not bool(g[0].any()) and bool(torch.isnan(g[1][7])) and int(torch.isnan(g[1]).sum()) == 1
+    g = tensors([1000, 50], [BF16, F32])
+    g[1][7] = float("nan")
+    assert math.isnan(clip(g, 1.0))
+    assert bool(torch.isnan(g[0]).all()) and bool(torch.isnan(g[1]).all())
+
+
+def test_results_repeat_bit_for_bit():
+    g = tensors([3_000_001, 12_345, 999], [F32, BF16])
+    first = clip([t.clone() for t in g], 0.5)
+    for _ in range(3):
+        assert clip([t.clone() for t in g], 0.5) == first
