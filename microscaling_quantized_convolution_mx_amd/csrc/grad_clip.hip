@@ -51,52 +51,58 @@ __device__ __forceinline__ int tensor_of(const Batch& b, int c) {
   return lo;
 }
 
+// Elements before the first multiple of 16 bytes (n at most).  Gradients that
+// are parts of a bucket start anywhere, so this is the usual case.
+template <class T>
+__device__ __forceinline__ int64_t head_of(const T* g, int64_t n) {
+  const int64_t h = static_cast<int64_t>((0 - reinterpret_cast<uintptr_t>(g)) % 16 / sizeof(T));
+  return h < n ? h : n;
+}
+
 template <class T>
 __device__ __forceinline__ double sum_chunk(const T* __restrict__ g, int64_t n) {
   constexpr int N = Pack<T>::N;
   double s = 0.0;
-  if (reinterpret_cast<uintptr_t>(g) % 16 == 0) {
-    const int64_t packs = n / N;
+  auto add = [&](float v) { s = __builtin_fma(static_cast<double>(v), static_cast<double>(v), s); };
+  const int64_t head = head_of(g, n), packs = (n - head) / N;
+  const uint4* v = reinterpret_cast<const uint4*>(g + head);
 #pragma unroll 4
-    for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
-      float x[N];
-      unpack<T>(reinterpret_cast<const uint4*>(g)[i], x);
+  for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
+    float x[N];
+    unpack<T>(v[i], x);
 #pragma unroll
-      for (int j = 0; j < N; ++j) s = __builtin_fma(static_cast<double>(x[j]), static_cast<double>(x[j]), s);
-    }
-    const int64_t i = packs * N + threadIdx.x;
-    if (i < n) {
-      const double x = to_f32(g[i]);
-      s = __builtin_fma(x, x, s);
-    }
-  } else {
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-      const double x = to_f32(g[i]);
-      s = __builtin_fma(x, x, s);
-    }
+    for (int j = 0; j < N; ++j) add(x[j]);
   }
+  // fewer than N elements before and after
+  const int64_t t = head + packs * N + threadIdx.x;
+  if (threadIdx.x < head) add(to_f32(g[threadIdx.x]));
+  if (t < n) add(to_f32(g[t]));
   return s;
 }
 
 template <class T>
 __device__ __forceinline__ void scale_chunk(const T* g, T* o, int64_t n, float f) {
   constexpr int N = Pack<T>::N;
-  int64_t done = 0;
-  if (reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
-    const int64_t packs = n / N;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
-      float x[N];
-      unpack<T>(reinterpret_cast<const uint4*>(g)[i], x);
-      uint4 w;
-      T* e = reinterpret_cast<T*>(&w);
-#pragma unroll
-      for (int j = 0; j < N; ++j) e[j] = from_f32<T>(x[j] * f);
-      reinterpret_cast<uint4*>(o)[i] = w;
-    }
-    done = packs * N;
+  if ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(o)) % 16 != 0) {
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) o[i] = from_f32<T>(to_f32(g[i]) * f);
+    return;
   }
-  for (int64_t i = done + threadIdx.x; i < n; i += kThreads) o[i] = from_f32<T>(to_f32(g[i]) * f);
+  const int64_t head = head_of(g, n), packs = (n - head) / N;
+  const uint4* v = reinterpret_cast<const uint4*>(g + head);
+  uint4* w = reinterpret_cast<uint4*>(o + head);
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < packs; i += kThreads) {
+    float x[N];
+    unpack<T>(v[i], x);
+    uint4 q;
+    T* e = reinterpret_cast<T*>(&q);
+#pragma unroll
+    for (int j = 0; j < N; ++j) e[j] = from_f32<T>(x[j] * f);
+    w[i] = q;
+  }
+  const int64_t t = head + packs * N + threadIdx.x;
+  if (threadIdx.x < head) o[threadIdx.x] = from_f32<T>(to_f32(g[threadIdx.x]) * f);
+  if (t < n) o[t] = from_f32<T>(to_f32(g[t]) * f);
 }
 
 // Sum over the workgroup, the same in every thread, in a fixed order.

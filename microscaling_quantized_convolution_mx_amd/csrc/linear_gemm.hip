@@ -17,6 +17,7 @@ namespace mx {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
@@ -32,12 +33,13 @@ __device__ __forceinline__ void static_for(F&& f) {
 struct ProductParams {
   const uint8_t *a, *as, *b, *bs;  // codes and scales
   void* out;
-  float* partial;          // split products: fp32 [splits][rows][cols] sums, else null
   int64_t akt, bkt;        // column tiles of a stripe
   int64_t bmat;            // ROWS: padded rows of one weight matrix in b
   int64_t a_rows, b_rows;  // padded rows of a and b (of all matrices)
   int64_t rows, cols;      // of out (ROWS: rows = tokens; CONTRACT: of one expert's matrix)
   int64_t ld;
+  int64_t split_out;       // elements of out from one piece of a split product to the next
+  int vec;                 // out's rows start at multiples of 16 bytes
   int ktiles;              // ROWS and one layer: column tiles to contract
   int tokens;
   const int32_t* offsets;
@@ -47,6 +49,66 @@ struct ProductParams {
 };
 
 __device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+
+// LDS that a wave's stores go through: 32 rows of its outputs, 16 bytes apart
+// from each other so that neither the writes nor the reads conflict.
+template <class U, int RM>
+__host__ __device__ constexpr int store_bytes() { return 32 * (RM * 32 * static_cast<int>(sizeof(U)) + 16); }
+
+// Stores the wave's RM x RM results.  The MFMA leaves lane l with row l%32
+// and 4 columns each at 8v + 4(l/32), v = 0..3: stored from there, a memory
+// instruction would write 32 short pieces.  Through LDS, 32 rows at a time,
+// it writes whole rows, 16 bytes per lane.
+// dst: the tile's first output; rleft, cleft: rows and columns from there on
+// that exist; vec: rows start at multiples of 16 bytes.
+template <int RM, class U>
+__device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RM], uint8_t* buf, U* dst, int64_t ld, bool vec, int64_t rleft,
+                                           int64_t cleft, int lane, int wm, int wn) {
+  constexpr int W = RM * 32;                                  // columns of the wave
+  constexpr int kRow = W * static_cast<int>(sizeof(U)) + 16;  // bytes between rows in LDS
+  constexpr int N = 16 / static_cast<int>(sizeof(U));         // elements of 16 bytes
+  constexpr int P = W / N;                                    // 16-byte pieces of a row
+  const int64_t c0 = wn * W;
+  cleft -= c0;
+  rleft -= wm * W;
+  dst += static_cast<int64_t>(wm * W) * ld + c0;
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+#pragma unroll
+    for (int j = 0; j < RM; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        struct alignas(4 * sizeof(U)) { U e[4]; } q;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) q.e[w] = from_f32<U>(acc[i][j][4 * v + w]);
+        __builtin_memcpy(__builtin_assume_aligned(buf + (lane & 31) * kRow + (32 * j + 8 * v + 4 * (lane >> 5)) * sizeof(U), 4 * sizeof(U)), &q, sizeof(q));
+      }
+    __builtin_amdgcn_wave_barrier();
+    U* d = dst + static_cast<int64_t>(32 * i) * ld;
+    const int64_t left = rleft - 32 * i;
+    if (vec) {
+#pragma unroll
+      for (int s = 0; s < 32 * P / 64; ++s) {
+        const int r = (s * 64 + lane) / P, c = (s * 64 + lane) % P * N;
+        const i32x4 q = *reinterpret_cast<const i32x4*>(buf + r * kRow + c * sizeof(U));
+        if (r < left) {
+          if (c + N <= cleft) *reinterpret_cast<i32x4*>(d + r * ld + c) = q;
+          else {
+            for (int e = 0; e < N; ++e)
+              if (c + e < cleft) d[r * ld + c + e] = reinterpret_cast<const U*>(buf + r * kRow + c * sizeof(U))[e];
+          }
+        }
+      }
+    } else {
+#pragma unroll 4
+      for (int s = 0; s < 32 * W / 64; ++s) {
+        const int r = (s * 64 + lane) / W, c = (s * 64 + lane) % W;
+        if (r < left && c < cleft) d[r * ld + c] = reinterpret_cast<const U*>(buf + r * kRow)[c];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
 
 // TILE x TILE outputs per workgroup, 4 waves of TILE/2 x TILE/2 in MFMAs of
 // 32x32x64.
@@ -143,9 +205,10 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     cleft = p.cols - static_cast<int64_t>(tj) * TILE;
   }
   int s_begin = 0, nsteps = ksteps;
-  if (p.partial) {
+  if (p.splits > 1) {
     s_begin = min(ksteps, sp * p.split_steps);
     nsteps = min(ksteps, s_begin + p.split_steps) - s_begin;
+    out += sp * p.split_out;
   }
   k0 += static_cast<int64_t>(s_begin) * kStepTiles;
 
@@ -244,7 +307,7 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
       constexpr int I = decltype(ic)::value;
       static_for<RM>([&](auto jc) {
         constexpr int J = decltype(jc)::value;
-        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.a[I], f.b[J], acc[I][J], 4, 4, I, f.sa, J, f.sb);
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (J == 0) {
           if (first) fetch_one(raw, fs, I);
@@ -287,43 +350,22 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     }
   }
 
-  // lane l holds column l%32 and rows 8(v/4) + 4(l/32) + v%4 of a 32x32
-  const int64_t tr = wm * (TILE / 2) + 4 * (lane >> 5), tc = wn * (TILE / 2) + (lane & 31);
-  if (p.partial) {
-    float* d = p.partial + (static_cast<int64_t>(sp) * p.rows + orow) * p.cols + static_cast<int64_t>(tj) * TILE;
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-      for (int j = 0; j < RM; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int64_t r = tr + 32 * i + 8 * (v / 4) + v % 4, c = tc + 32 * j;
-          if (r < rleft && c < cleft) d[r * p.cols + c] = acc[i][j][v];
-        }
-    return;
-  }
-  T* d = out + orow * p.ld + static_cast<int64_t>(tj) * TILE;
-#pragma unroll
-  for (int i = 0; i < RM; ++i)
-#pragma unroll
-    for (int j = 0; j < RM; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t r = tr + 32 * i + 8 * (v / 4) + v % 4, c = tc + 32 * j;
-        if (r < rleft && c < cleft) d[r * p.ld + c] = from_f32<T>(acc[i][j][v]);
-      }
+  store_wave<RM>(acc, lds + wave * store_bytes<T, RM>(), out + orow * p.ld + static_cast<int64_t>(tj) * TILE, p.ld, p.vec != 0, rleft, cleft,
+                 lane, wm, wn);
 }
 
-// Sums the pieces of a split product in their order.
+// Sums the pieces of a split product in their order, 4 columns per thread.
 template <class T>
 __global__ __launch_bounds__(256) void k_lin_reduce(const float* __restrict__ partial, int splits, int64_t rows, int64_t cols,
-                                                     T* __restrict__ out, int64_t ld) {
-  const int64_t n = rows * cols;
+                                                     int64_t pcols, T* __restrict__ out, int64_t ld) {
+  const int64_t n = rows * pcols / 4;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
-    float s = partial[i];
-    for (int q = 1; q < splits; ++q) s += partial[q * n + i];
-    const int64_t r = i / cols;
-    out[r * ld + (i - r * cols)] = from_f32<T>(s);
+    f32x4 s = reinterpret_cast<const f32x4*>(partial)[i];
+    for (int q = 1; q < splits; ++q) s += reinterpret_cast<const f32x4*>(partial)[q * n + i];
+    const int64_t r = 4 * i / pcols, c = 4 * i - r * pcols;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < cols) out[r * ld + c + e] = from_f32<T>(s[e]);
   }
 }
 
@@ -370,7 +412,7 @@ size_t lin_product_workspace(const LinGeom& g, LinOp op) {
   const Plan pl = make_plan(g, op);
   if (pl.splits <= 1) return 0;
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
-  return static_cast<size_t>(pl.splits * rows * cols) * sizeof(float);
+  return static_cast<size_t>(pl.splits * rows * ((cols + 3) / 4 * 4)) * sizeof(float);
 }
 
 hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
@@ -394,8 +436,15 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.b_rows = p.bmat * form_matrices(g, rb);
   p.rows = op == LIN_WGRAD ? g.n : g.m;
   p.cols = op == LIN_FWD ? g.n : g.k;
-  p.out = out;
-  p.ld = ld;
+  // a split product leaves fp32 sums in the workspace, with rows of whole 16
+  // bytes, for k_lin_reduce
+  const bool split = pl.splits > 1;
+  const int64_t pcols = (p.cols + 3) / 4 * 4;
+  p.out = split ? workspace : out;
+  p.ld = split ? pcols : ld;
+  p.split_out = p.rows * pcols;
+  const int64_t size = split || dtype == MX_F32 ? 4 : 2;
+  p.vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld * size % 16 == 0;
   p.tokens = static_cast<int>(g.m);
   p.offsets = offsets;
   p.experts = g.e;
@@ -403,17 +452,25 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.tiles_j = static_cast<int>(pl.tiles_j);
   p.splits = pl.splits;
   p.split_steps = pl.split_steps;
-  p.partial = pl.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   const unsigned grid = static_cast<unsigned>((pl.units * pl.splits + 7) / 8 * 8);
-  auto go = [&](auto t) {
+  auto multiply = [&](auto t) {
     using T = decltype(t);
     auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, s, p); };
     if (op == LIN_WGRAD) pl.tile == 256 ? launch(k_lin_product<T, 256, true>) : launch(k_lin_product<T, 128, true>);
     else pl.tile == 256 ? launch(k_lin_product<T, 256, false>) : launch(k_lin_product<T, 128, false>);
-    if (pl.splits > 1) {
-      const int64_t n = p.rows * p.cols;
-      const unsigned wgs = static_cast<unsigned>(n / 256 < 2048 ? (n + 255) / 256 : 2048);
-      hipLaunchKernelGGL(k_lin_reduce<T>, dim3(wgs), dim3(256), 0, s, p.partial, p.splits, p.rows, p.cols, static_cast<T*>(out), ld);
+  };
+  auto reduce = [&](auto t) {
+    using T = decltype(t);
+    const int64_t n = p.rows * pcols / 4;
+    const unsigned wgs = static_cast<unsigned>(n / 256 < 2048 ? (n + 255) / 256 : 2048);
+    hipLaunchKernelGGL(k_lin_reduce<T>, dim3(wgs), dim3(256), 0, s, static_cast<const float*>(workspace), p.splits, p.rows, p.cols, pcols,
+                       static_cast<T*>(out), ld);
+  };
+  auto go = [&](auto t) {
+    if (!split) multiply(t);
+    else {
+      multiply(float{});
+      reduce(t);
     }
   };
   switch (dtype) {
