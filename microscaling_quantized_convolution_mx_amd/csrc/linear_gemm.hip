@@ -234,34 +234,35 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     int sa, sb;
   };
   Raw r0, r1;
-  // a step past the last one reads the last one again
-  auto fetch_one = [&](Raw& raw, int step, int q) {
-    const int64_t o = static_cast<int64_t>(min(step, nsteps - 1)) * (kStepTiles * kTileBytes);
-    raw.a[q] = reinterpret_cast<const i32x4*>(asrc[q] + o)[lane];
-    raw.b[q] = reinterpret_cast<const i32x4*>(bsrc[q] + o)[lane];
-  };
-  auto fetch_scales = [&](Raw& raw, int step) {
-    const int64_t o = static_cast<int64_t>(min(step, nsteps - 1)) * (kStepTiles * kScaleBytes);
-    raw.sa = reinterpret_cast<const int*>(assrc + o)[lane];
-    raw.sb = reinterpret_cast<const int*>(bssrc + o)[lane];
-  };
-  auto fetch = [&](Raw& raw, int step) {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) fetch_one(raw, step, q);
-    fetch_scales(raw, step);
-  };
-  // ... and is written with zeros for a's codes.  (A scale that is NaN has
-  // already made those sums NaN.)
-  auto stage_write = [&](const Raw& raw, uint8_t* st, int step) {
-    const int m = step < nsteps ? -1 : 0;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      reinterpret_cast<i32x4*>(st)[q * 256 + tid] = raw.a[q] & m;
-      reinterpret_cast<i32x4*>(st + kOpnd)[q * 256 + tid] = raw.b[q];
+  // load l of a step: a and b pieces in turn, then the scales.  A step past
+  // the last one reads the last one again ...
+  constexpr int kLoads = 2 * NQ + 2;
+  auto load = [&](Raw& raw, int step, auto l) {
+    constexpr int L = decltype(l)::value;
+    const int64_t st = min(step, nsteps - 1);
+    if constexpr (L < 2 * NQ) {
+      const uint8_t* src = (L % 2 ? bsrc[L / 2] : asrc[L / 2]) + st * (kStepTiles * kTileBytes);
+      (L % 2 ? raw.b[L / 2] : raw.a[L / 2]) = reinterpret_cast<const i32x4*>(src)[lane];
+    } else {
+      const uint8_t* src = (L % 2 ? bssrc : assrc) + st * (kStepTiles * kScaleBytes);
+      (L % 2 ? raw.sb : raw.sa) = reinterpret_cast<const int*>(src)[lane];
     }
-    if (scaler) {
-      reinterpret_cast<int*>(st + 2 * kOpnd)[tid] = raw.sa;
-      reinterpret_cast<int*>(st + 2 * kOpnd + kOpndS)[tid] = raw.sb;
+  };
+  // ... and write w of it puts zeros in place of a's codes.  (A scale that is
+  // NaN has already made those sums NaN.)
+  constexpr int kWrites = 2 * NQ + 1;
+  auto write = [&](const Raw& raw, uint8_t* st, int step, auto w) {
+    constexpr int W = decltype(w)::value;
+    if constexpr (W == 2 * NQ) {
+      if (scaler) {
+        reinterpret_cast<int*>(st + 2 * kOpnd)[tid] = raw.sa;
+        reinterpret_cast<int*>(st + 2 * kOpnd + kOpndS)[tid] = raw.sb;
+      }
+    } else if constexpr (W % 2 == 0) {
+      const int m = step < nsteps ? -1 : 0;
+      reinterpret_cast<i32x4*>(st)[W / 2 * 256 + tid] = raw.a[W / 2] & m;
+    } else {
+      reinterpret_cast<i32x4*>(st + kOpnd)[W / 2 * 256 + tid] = raw.b[W / 2];
     }
   };
 
@@ -278,53 +279,82 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     int sa, sb;
   };
   Frags fA, fB;
-  auto read_frags = [&](const uint8_t* st, int j, Frags& f) {
-    // a wave of 64 rows uses two bytes of its 128 rows' scales
-    const uint8_t* s = st + 2 * kOpnd;
-    if constexpr (RM == 4) {
-      f.sa = reinterpret_cast<const int*>(s + (wm * kStepTiles + j) * kScaleBytes)[lane];
-      f.sb = reinterpret_cast<const int*>(s + kOpndS + (wn * kStepTiles + j) * kScaleBytes)[lane];
+  // read r of slice j: the scales, then the tiles in the order of their use
+  constexpr int kReads = 2 * RM + 2;
+  auto read = [&](const uint8_t* st, int j, Frags& f, auto r) {
+    constexpr int R = decltype(r)::value;
+    if constexpr (R < 2) {
+      // a wave of 64 rows uses two bytes of its 128 rows' scales
+      const uint8_t* s = st + 2 * kOpnd + R * kOpndS;
+      const int w = R ? wn : wm;
+      (R ? f.sb : f.sa) = RM == 4 ? reinterpret_cast<const int*>(s + (w * kStepTiles + j) * kScaleBytes)[lane]
+                                  : reinterpret_cast<const uint16_t*>(s + j * kScaleBytes)[2 * lane + w];
+    } else if constexpr (R == 2 || R >= RM + 3) {
+      constexpr int I = R == 2 ? 0 : R - RM - 2;
+      f.a[I] = operand(reinterpret_cast<const i32x4*>(st + ((wm * RM + I) * kStepTiles + j) * kTileBytes)[lane]);
     } else {
-      f.sa = reinterpret_cast<const uint16_t*>(s + j * kScaleBytes)[2 * lane + wm];
-      f.sb = reinterpret_cast<const uint16_t*>(s + kOpndS + j * kScaleBytes)[2 * lane + wn];
-    }
-#pragma unroll
-    for (int i = 0; i < RM; ++i) {
-      f.a[i] = operand(reinterpret_cast<const i32x4*>(st + ((wm * RM + i) * kStepTiles + j) * kTileBytes)[lane]);
-      f.b[i] = operand(reinterpret_cast<const i32x4*>(st + kOpnd + ((wn * RM + i) * kStepTiles + j) * kTileBytes)[lane]);
+      constexpr int I = R - 3;
+      f.b[I] = operand(reinterpret_cast<const i32x4*>(st + kOpnd + ((wn * RM + I) * kStepTiles + j) * kTileBytes)[lane]);
     }
   };
 
-  // Step s, on stage s%3, with slice 0's operands read during step s-1: write
-  // step s+2 (fetched two steps ago) into stage (s+2)%3, whose last reads
-  // were in step s-1; read slice 1; multiply slice 0, fetching step s+4
-  // between the MFMAs; read slice 0 of step s+1, complete since the barrier
-  // of step s-1; multiply slice 1; barrier.  Steps run in pairs so that the
-  // two register sets alternate statically; the extra step of an odd count
-  // multiplies zeros.
-  auto slice = [&](const Frags& f, Raw& raw, int fs, bool first) {
-    static_for<RM>([&](auto ic) {
-      constexpr int I = decltype(ic)::value;
-      static_for<RM>([&](auto jc) {
-        constexpr int J = decltype(jc)::value;
-        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (J == 0) {
-          if (first) fetch_one(raw, fs, I);
-          else if (I == 0) fetch_scales(raw, fs);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      });
-    });
+  // Step s, on stage s%3, with slice 0's operands read during step s-1:
+  //   multiply slice 0, reading slice 1 and starting to write step s+2
+  //   (loaded two steps ago) into stage (s+2)%3, whose last reads were in
+  //   step s-1;
+  //   multiply slice 1, reading slice 0 of step s+1, complete since the
+  //   barrier of step s-1, writing the rest and loading step s+4 into the
+  //   registers that the writes have freed;
+  //   barrier.
+  // With one wave per SIMD nothing else hides an LDS access, so they are
+  // dealt out between the MFMAs: an MFMA lasts 32 cycles, in which LDS serves
+  // about one 1 KiB access of each of the four waves.  (All of a slice's
+  // accesses ahead of its MFMAs: see the kernel's figures below.)  Steps run in
+  // pairs so that the two register sets alternate statically; the extra step
+  // of an odd count multiplies zeros.
+  constexpr int kSlots = RM * RM;
+  constexpr int kPerSlot = RM == 4 ? 1 : 2;         // reads after an MFMA
+  constexpr int kReadSlots = kReads / kPerSlot;     // MFMAs with reads after them
+  constexpr int kEarly = RM == 4 ? 5 : 3;           // writes during slice 0
+  constexpr int kWriteSlots = kSlots - kReadSlots;
+  static_assert(kReads % kPerSlot == 0 && kWriteSlots > 0 && kEarly < kWrites);
+  auto mfma = [&](const Frags& f, auto n) {
+    constexpr int I = decltype(n)::value / RM, J = decltype(n)::value % RM;
+    acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
+    __builtin_amdgcn_sched_barrier(0);
   };
+  // items [begin, end) of `count` that slot i of n takes, `each` per slot and
+  // the rest with the last slot
+  auto deal = [](int i, int n, int count) constexpr { return i >= n ? count : i * count / n; };
   auto step = [&](int s, const uint8_t* cur, const uint8_t* next, uint8_t* to, Raw& raw) {
-    stage_write(raw, to, s + 2);
-    read_frags(cur, 1, fB);
-    __builtin_amdgcn_sched_barrier(0);
-    slice(fA, raw, s + 4, true);
-    read_frags(next, 0, fA);
-    __builtin_amdgcn_sched_barrier(0);
-    slice(fB, raw, s + 4, false);
+    static_for<kSlots>([&](auto n) {
+      constexpr int N = decltype(n)::value;
+      mfma(fA, n);
+      if constexpr (N < kReadSlots) {
+        static_for<kPerSlot>([&](auto i) { read(cur, 1, fB, Idx<N * kPerSlot + decltype(i)::value>{}); });
+      } else {
+        constexpr int B = deal(N - kReadSlots, kWriteSlots, kEarly), E = deal(N - kReadSlots + 1, kWriteSlots, kEarly);
+        static_for<E - B>([&](auto i) { write(raw, to, s + 2, Idx<B + decltype(i)::value>{}); });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    static_for<kSlots>([&](auto n) {
+      constexpr int N = decltype(n)::value;
+      mfma(fB, n);
+      if constexpr (N < kReadSlots) {
+        static_for<kPerSlot>([&](auto i) { read(next, 0, fA, Idx<N * kPerSlot + decltype(i)::value>{}); });
+        constexpr int B = deal(N, kReadSlots, kEarly), E = deal(N + 1, kReadSlots, kEarly);
+        static_for<E - B>([&](auto i) { load(raw, s + 4, Idx<B + decltype(i)::value>{}); });
+      } else {
+        constexpr int C = kWrites - kEarly, D = kLoads - kEarly;
+        constexpr int B = deal(N - kReadSlots, kWriteSlots, C), E = deal(N - kReadSlots + 1, kWriteSlots, C);
+        static_for<E - B>([&](auto i) { write(raw, to, s + 2, Idx<kEarly + B + decltype(i)::value>{}); });
+        // a load follows the write of the register it fills
+        constexpr int LE = E == C ? D : E, LB = B == C ? D : B;
+        static_for<LE - LB>([&](auto i) { load(raw, s + 4, Idx<kEarly + LB + decltype(i)::value>{}); });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
     // keeps the MFMAs ahead of the barrier
 #pragma unroll
     for (int i = 0; i < RM; ++i)
@@ -333,14 +363,21 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     __syncthreads();
   };
   if (nsteps > 0) {
-    fetch(r0, 0);
-    fetch(r1, 1);
-    stage_write(r0, lds, 0);
-    stage_write(r1, lds + kStage, 1);
-    fetch(r0, 2);
-    fetch(r1, 3);
+    // the loop waits for its loads by their number, so here too they have to
+    // be issued in the loop's order
+    auto load_all = [&](Raw& raw, int step) {
+      static_for<kLoads>([&](auto l) { load(raw, step, l); });
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    load_all(r0, 0);
+    load_all(r1, 1);
+    static_for<kWrites>([&](auto w) { write(r0, lds, 0, w); });
+    static_for<kWrites>([&](auto w) { write(r1, lds + kStage, 1, w); });
+    __builtin_amdgcn_sched_barrier(0);
+    load_all(r0, 2);
+    load_all(r1, 3);
     __syncthreads();
-    read_frags(lds, 0, fA);
+    static_for<kReads>([&](auto r) { read(lds, 0, fA, r); });
     int c = 0;
     for (int s = 0; s < nsteps; s += 2) {
       const int c1 = c == 2 ? 0 : c + 1, c2 = c1 == 2 ? 0 : c1 + 1;
