@@ -50,6 +50,13 @@ struct ProductParams {
 
 __device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
 
+// A value that all lanes have alike.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(static_cast<uint64_t>(v) >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // LDS that a wave's stores go through: 32 rows of its outputs, 16 bytes apart
 // from each other so that neither the writes nor the reads conflict.
 template <class U, int RM>
@@ -110,23 +117,47 @@ __device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RM], uint8_t*
   }
 }
 
+// Copies BYTES per lane from src + lane * BYTES to the LDS address dst + lane *
+// BYTES without passing registers.  src and dst are the wave's.  The compiler
+// does not know of the copy (told of it, it would wait for all copies on
+// their way before any LDS read), so whoever reads the data waits for it with
+// wait_barrier.  There is no output register, and the address registers are
+// read when the instruction issues.
+template <int BYTES>
+__device__ __forceinline__ void copy_lds(const uint8_t* src, uint32_t dst, int lane) {
+  const uint32_t off = static_cast<uint32_t>(lane) * BYTES;
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(dst), "v"(off), "s"(src) : "memory");
+}
+
+// Waits until at most N of the wave's copies and none of its LDS reads are on
+// their way, then for the workgroup's other waves to have come as far.
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+  static_assert(N < 64);
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // TILE x TILE outputs per workgroup, 4 waves of TILE/2 x TILE/2 in MFMAs of
-// 32x32x64.
-//
-// One step contracts 128 columns: two MFMA slices.  Each thread copies
-// 16-byte pieces of the operands' tiles from memory into one of three LDS
-// stages, in the order they are stored: the pieces are fetched into registers
-// two steps before they are written to LDS, which happens two steps before
-// they are read.  A tile in LDS is read as it is, 64 lanes x 16 consecutive
-// bytes, which is free of bank conflicts.
+// 32x32x64.  One step contracts 128 columns: two MFMA slices.  A tile in LDS
+// is read as it is, 64 lanes x 16 consecutive bytes, which is free of bank
+// conflicts.
 template <class T, int TILE, bool CONTRACT>
 __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
   constexpr int RM = TILE / 64;               // MFMA rows and columns of a wave
-  constexpr int NQ = TILE / 64;               // 16-byte pieces a thread copies per operand and step
+  constexpr int NQ = TILE / 64;               // tiles a wave copies per operand and step
   constexpr int kOpnd = (TILE / 32) * kStepTiles * kTileBytes;
   constexpr int kOpndS = (TILE / 128) * kStepTiles * kScaleBytes;
+  constexpr int NS = TILE / 128;              // 256-byte groups of scales a wave copies per step
   constexpr int kStage = 2 * kOpnd + 2 * kOpndS;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage];
+  constexpr int kStages = 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -211,11 +242,22 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     out += sp * p.split_out;
   }
   k0 += static_cast<int64_t>(s_begin) * kStepTiles;
+  // what the experts' offsets say is the same in all lanes: in scalar registers from here on
+  arow = uniform(arow);
+  brow = uniform(brow);
+  orow = uniform(orow);
+  rleft = uniform(rleft);
+  k0 = uniform(k0);
+  nsteps = __builtin_amdgcn_readfirstlane(nsteps);
 
-  // Copy: wave w's piece q is tile w%2 of stripe 2q + w/2.  A stripe past the
-  // operand's end is read as its last one: those outputs are not stored.
-  const uint8_t* asrc[NQ];
-  const uint8_t* bsrc[NQ];
+  // Copies.  A step's tiles go from memory to LDS as they are stored, without
+  // passing registers: wave w's copy q takes tile w%2 of stripe 2q + w/2 of
+  // an operand, 64 lanes x 16 bytes, and one of the scales' 256-byte groups
+  // (for 256 rows of an operand one of a, one of b; for 128 rows the waves
+  // take a's two and b's two).  A stripe past the operand's end is read as
+  // its last one: those outputs are not stored.
+  const uint8_t *asrc[NQ], *bsrc[NQ], *ssrc[NS];
+  uint32_t sdst[NS];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const int64_t st = 2 * q + (wave >> 1);
@@ -223,47 +265,34 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     asrc[q] = p.a + (sa * p.akt + k0 + (wave & 1)) * kTileBytes;
     bsrc[q] = p.b + (sb * p.bkt + k0 + (wave & 1)) * kTileBytes;
   }
-  // scales: dword t of a step is lane t%64 of tile (t/64)%2 of the 128 rows t/128
-  const bool scaler = TILE == 256 || tid < 128;
-  const int64_t ga = min(arow / kPad + (wave >> 1), p.a_rows / kPad - 1), gb = min(brow / kPad + (wave >> 1), p.b_rows / kPad - 1);
-  const uint8_t* assrc = p.as + (ga * p.akt + k0 + (wave & 1)) * kScaleBytes;
-  const uint8_t* bssrc = p.bs + (gb * p.bkt + k0 + (wave & 1)) * kScaleBytes;
-
-  struct Raw {
-    i32x4 a[NQ], b[NQ];
-    int sa, sb;
-  };
-  Raw r0, r1;
-  // load l of a step: a and b pieces in turn, then the scales.  A step past
-  // the last one reads the last one again ...
-  constexpr int kLoads = 2 * NQ + 2;
-  auto load = [&](Raw& raw, int step, auto l) {
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const bool of_b = NS == 2 ? i == 1 : (wave >> 1) == 1;
+    const int64_t g = NS == 2 ? wave >> 1 : 0;  // 128 rows of the tile
+    const int64_t r = min((of_b ? brow : arow) / kPad + g, (of_b ? p.b_rows : p.a_rows) / kPad - 1);
+    ssrc[i] = (of_b ? p.bs : p.as) + (r * (of_b ? p.bkt : p.akt) + k0 + (wave & 1)) * kScaleBytes;
+    sdst[i] = 2 * kOpnd + (of_b ? kOpndS : 0) + static_cast<uint32_t>(g * kStepTiles + (wave & 1)) * kScaleBytes;
+  }
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  // copy l of the step that the sources stand at, into the stage at `to`
+  constexpr int kCopies = 2 * NQ + NS;
+  auto copy = [&](uint32_t to, auto l) {
     constexpr int L = decltype(l)::value;
-    const int64_t st = min(step, nsteps - 1);
     if constexpr (L < 2 * NQ) {
-      const uint8_t* src = (L % 2 ? bsrc[L / 2] : asrc[L / 2]) + st * (kStepTiles * kTileBytes);
-      (L % 2 ? raw.b[L / 2] : raw.a[L / 2]) = reinterpret_cast<const i32x4*>(src)[lane];
+      copy_lds<16>(L % 2 ? bsrc[L / 2] : asrc[L / 2], lds0 + to + (L % 2 ? kOpnd : 0) + (L / 2) * 4096 + wave * kTileBytes, lane);
     } else {
-      const uint8_t* src = (L % 2 ? bssrc : assrc) + st * (kStepTiles * kScaleBytes);
-      (L % 2 ? raw.sb : raw.sa) = reinterpret_cast<const int*>(src)[lane];
+      copy_lds<4>(ssrc[L - 2 * NQ], lds0 + to + sdst[L - 2 * NQ], lane);
     }
   };
-  // ... and write w of it puts zeros in place of a's codes.  (A scale that is
-  // NaN has already made those sums NaN.)
-  constexpr int kWrites = 2 * NQ + 1;
-  auto write = [&](const Raw& raw, uint8_t* st, int step, auto w) {
-    constexpr int W = decltype(w)::value;
-    if constexpr (W == 2 * NQ) {
-      if (scaler) {
-        reinterpret_cast<int*>(st + 2 * kOpnd)[tid] = raw.sa;
-        reinterpret_cast<int*>(st + 2 * kOpnd + kOpndS)[tid] = raw.sb;
-      }
-    } else if constexpr (W % 2 == 0) {
-      const int m = step < nsteps ? -1 : 0;
-      reinterpret_cast<i32x4*>(st)[W / 2 * 256 + tid] = raw.a[W / 2] & m;
-    } else {
-      reinterpret_cast<i32x4*>(st + kOpnd)[W / 2 * 256 + tid] = raw.b[W / 2];
+  auto advance = [&](bool on) {
+    const int d = on ? 1 : 0;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      asrc[q] += d * (kStepTiles * kTileBytes);
+      bsrc[q] += d * (kStepTiles * kTileBytes);
     }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) ssrc[i] += d * (kStepTiles * kScaleBytes);
   };
 
   f32x16 acc[RM][RM];
@@ -298,93 +327,58 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     }
   };
 
-  // Step s, on stage s%3, with slice 0's operands read during step s-1:
-  //   multiply slice 0, reading slice 1 and starting to write step s+2
-  //   (loaded two steps ago) into stage (s+2)%3, whose last reads were in
-  //   step s-1;
-  //   multiply slice 1, reading slice 0 of step s+1, complete since the
-  //   barrier of step s-1, writing the rest and loading step s+4 into the
-  //   registers that the writes have freed;
-  //   barrier.
-  // With one wave per SIMD nothing else hides an LDS access, so they are
-  // dealt out between the MFMAs: an MFMA lasts 32 cycles, in which LDS serves
-  // about one 1 KiB access of each of the four waves.  (All of a slice's
-  // accesses ahead of its MFMAs: see the kernel's figures below.)  Steps run in
-  // pairs so that the two register sets alternate statically; the extra step
-  // of an odd count multiplies zeros.
+  // Step s, on stage s%4, with slice 0's operands read during step s-1:
+  //   multiply slice 0, reading slice 1;
+  //   barrier: every wave has read all of stage s%4, and its copies of step
+  //   s+1 have arrived (those of steps s+2 and s+3 may be on their way);
+  //   multiply slice 1, reading slice 0 of step s+1 and copying step s+4 into
+  //   stage s%4, three steps ahead of its use.
+  // With one wave per SIMD nothing else hides an LDS access, so reads and
+  // copies are dealt out between the MFMAs: an MFMA lasts 32 cycles, in which
+  // LDS serves about one 1 KiB access of each of the four waves.  Copies past
+  // the last step repeat it, into stages that nothing reads.
   constexpr int kSlots = RM * RM;
-  constexpr int kPerSlot = RM == 4 ? 1 : 2;         // reads after an MFMA
-  constexpr int kReadSlots = kReads / kPerSlot;     // MFMAs with reads after them
-  constexpr int kEarly = RM == 4 ? 5 : 3;           // writes during slice 0
-  constexpr int kWriteSlots = kSlots - kReadSlots;
-  static_assert(kReads % kPerSlot == 0 && kWriteSlots > 0 && kEarly < kWrites);
   auto mfma = [&](const Frags& f, auto n) {
     constexpr int I = decltype(n)::value / RM, J = decltype(n)::value % RM;
     acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // items [begin, end) of `count` that slot i of n takes, `each` per slot and
-  // the rest with the last slot
-  auto deal = [](int i, int n, int count) constexpr { return i >= n ? count : i * count / n; };
-  auto step = [&](int s, const uint8_t* cur, const uint8_t* next, uint8_t* to, Raw& raw) {
-    static_for<kSlots>([&](auto n) {
-      constexpr int N = decltype(n)::value;
-      mfma(fA, n);
-      if constexpr (N < kReadSlots) {
-        static_for<kPerSlot>([&](auto i) { read(cur, 1, fB, Idx<N * kPerSlot + decltype(i)::value>{}); });
-      } else {
-        constexpr int B = deal(N - kReadSlots, kWriteSlots, kEarly), E = deal(N - kReadSlots + 1, kWriteSlots, kEarly);
-        static_for<E - B>([&](auto i) { write(raw, to, s + 2, Idx<B + decltype(i)::value>{}); });
-      }
-      __builtin_amdgcn_sched_barrier(0);
+  // the items of `count` that follow MFMA n when they are dealt out over a slice
+  auto deal = [&](auto n, auto count, auto&& f) {
+    constexpr int N = decltype(n)::value, C = decltype(count)::value;
+    constexpr int kEach = (C + kSlots - 1) / kSlots;
+    static_for<kEach>([&](auto i) {
+      constexpr int X = N * kEach + decltype(i)::value;
+      if constexpr (X < C) f(Idx<X>{});
     });
-    static_for<kSlots>([&](auto n) {
-      constexpr int N = decltype(n)::value;
-      mfma(fB, n);
-      if constexpr (N < kReadSlots) {
-        static_for<kPerSlot>([&](auto i) { read(next, 0, fA, Idx<N * kPerSlot + decltype(i)::value>{}); });
-        constexpr int B = deal(N, kReadSlots, kEarly), E = deal(N + 1, kReadSlots, kEarly);
-        static_for<E - B>([&](auto i) { load(raw, s + 4, Idx<B + decltype(i)::value>{}); });
-      } else {
-        constexpr int C = kWrites - kEarly, D = kLoads - kEarly;
-        constexpr int B = deal(N - kReadSlots, kWriteSlots, C), E = deal(N - kReadSlots + 1, kWriteSlots, C);
-        static_for<E - B>([&](auto i) { write(raw, to, s + 2, Idx<kEarly + B + decltype(i)::value>{}); });
-        // a load follows the write of the register it fills
-        constexpr int LE = E == C ? D : E, LB = B == C ? D : B;
-        static_for<LE - LB>([&](auto i) { load(raw, s + 4, Idx<kEarly + LB + decltype(i)::value>{}); });
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    });
-    // keeps the MFMAs ahead of the barrier
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-      for (int j = 0; j < RM; ++j) asm volatile("" : "+a"(acc[i][j]));
-    __syncthreads();
   };
   if (nsteps > 0) {
-    // the loop waits for its loads by their number, so here too they have to
-    // be issued in the loop's order
-    auto load_all = [&](Raw& raw, int step) {
-      static_for<kLoads>([&](auto l) { load(raw, step, l); });
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    load_all(r0, 0);
-    load_all(r1, 1);
-    static_for<kWrites>([&](auto w) { write(r0, lds, 0, w); });
-    static_for<kWrites>([&](auto w) { write(r1, lds + kStage, 1, w); });
-    __builtin_amdgcn_sched_barrier(0);
-    load_all(r0, 2);
-    load_all(r1, 3);
-    __syncthreads();
+    static_for<kStages>([&](auto st) {
+      static_for<kCopies>([&](auto l) { copy(decltype(st)::value * kStage, l); });
+      advance(decltype(st)::value + 1 < nsteps);
+    });
+    wait_barrier<(kStages - 1) * kCopies>();
     static_for<kReads>([&](auto r) { read(lds, 0, fA, r); });
-    int c = 0;
-    for (int s = 0; s < nsteps; s += 2) {
-      const int c1 = c == 2 ? 0 : c + 1, c2 = c1 == 2 ? 0 : c1 + 1;
-      step(s, lds + c * kStage, lds + c1 * kStage, lds + c2 * kStage, r0);
-      step(s + 1, lds + c1 * kStage, lds + c2 * kStage, lds + c * kStage, r1);
-      c = c2;
+    uint32_t cur = 0;
+    for (int s = 0; s < nsteps; ++s) {
+      const uint32_t next = cur == (kStages - 1) * kStage ? 0 : cur + kStage;
+      static_for<kSlots>([&](auto n) {
+        mfma(fA, n);
+        deal(n, Idx<kReads>{}, [&](auto r) { read(lds + cur, 1, fB, r); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      wait_barrier<(kStages - 2) * kCopies>();
+      static_for<kSlots>([&](auto n) {
+        mfma(fB, n);
+        deal(n, Idx<kReads>{}, [&](auto r) { read(lds + next, 0, fA, r); });
+        deal(n, Idx<kCopies>{}, [&](auto l) { copy(cur, l); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      advance(s + kStages + 1 < nsteps);
+      cur = next;
     }
+    // the last copies have to land before the stores reuse LDS
+    wait_barrier<0>();
   }
 
   store_wave<RM>(acc, lds + wave * store_bytes<T, RM>(), out + orow * p.ld + static_cast<int64_t>(tj) * TILE, p.ld, p.vec != 0, rleft, cleft,
