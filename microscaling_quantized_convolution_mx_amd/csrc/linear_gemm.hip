@@ -328,11 +328,12 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
   };
 
   // Step s, on stage s%4, with slice 0's operands read during step s-1:
-  //   multiply slice 0, reading slice 1;
+  //   multiply slice 0, reading slice 1 and copying the second half of step
+  //   s+3 into stage (s+3)%4;
   //   barrier: every wave has read all of stage s%4, and its copies of step
   //   s+1 have arrived (those of steps s+2 and s+3 may be on their way);
-  //   multiply slice 1, reading slice 0 of step s+1 and copying step s+4 into
-  //   stage s%4, three steps ahead of its use.
+  //   multiply slice 1, reading slice 0 of step s+1 and copying the first
+  //   half of step s+4 into stage s%4.
   // With one wave per SIMD nothing else hides an LDS access, so reads and
   // copies are dealt out between the MFMAs: an MFMA lasts 32 cycles, in which
   // LDS serves about one 1 KiB access of each of the four waves.  Copies past
@@ -343,38 +344,44 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // the items of `count` that follow MFMA n when they are dealt out over a slice
-  auto deal = [&](auto n, auto count, auto&& f) {
-    constexpr int N = decltype(n)::value, C = decltype(count)::value;
-    constexpr int kEach = (C + kSlots - 1) / kSlots;
-    static_for<kEach>([&](auto i) {
-      constexpr int X = N * kEach + decltype(i)::value;
-      if constexpr (X < C) f(Idx<X>{});
-    });
+  // items first .. first+count-1 dealt out evenly over a slice's first `span`
+  // MFMAs: those that follow MFMA n
+  auto deal = [&](auto n, auto first, auto count, auto span, auto&& f) {
+    constexpr int N = decltype(n)::value, C = decltype(count)::value, S = decltype(span)::value;
+    constexpr int B = N < S ? (N * C + S - 1) / S : C, E = N + 1 < S ? ((N + 1) * C + S - 1) / S : C;
+    static_for<E - B>([&](auto i) { f(Idx<decltype(first)::value + B + decltype(i)::value>{}); });
   };
+  constexpr int kHalf = kCopies / 2;
   if (nsteps > 0) {
     static_for<kStages>([&](auto st) {
-      static_for<kCopies>([&](auto l) { copy(decltype(st)::value * kStage, l); });
-      advance(decltype(st)::value + 1 < nsteps);
+      // the last stage's second half follows in the loop
+      constexpr int S = decltype(st)::value;
+      static_for<S + 1 < kStages ? kCopies : kHalf>([&](auto l) { copy(S * kStage, l); });
+      if constexpr (S + 1 < kStages) advance(S + 1 < nsteps);
     });
-    wait_barrier<(kStages - 1) * kCopies>();
-    static_for<kReads>([&](auto r) { read(lds, 0, fA, r); });
-    uint32_t cur = 0;
+    wait_barrier<(kStages - 2) * kCopies + kHalf>();
+    static_for<kReads>([&](auto r) {
+      read(lds, 0, fA, r);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    uint32_t cur = 0, last = (kStages - 1) * kStage;
     for (int s = 0; s < nsteps; ++s) {
       const uint32_t next = cur == (kStages - 1) * kStage ? 0 : cur + kStage;
       static_for<kSlots>([&](auto n) {
         mfma(fA, n);
-        deal(n, Idx<kReads>{}, [&](auto r) { read(lds + cur, 1, fB, r); });
+        deal(n, Idx<0>{}, Idx<kReads>{}, Idx<kSlots * 3 / 4>{}, [&](auto r) { read(lds + cur, 1, fB, r); });
+        deal(n, Idx<kHalf>{}, Idx<kCopies - kHalf>{}, Idx<kSlots>{}, [&](auto l) { copy(last, l); });
         __builtin_amdgcn_sched_barrier(0);
       });
+      advance(s + kStages < nsteps);
       wait_barrier<(kStages - 2) * kCopies>();
       static_for<kSlots>([&](auto n) {
         mfma(fB, n);
-        deal(n, Idx<kReads>{}, [&](auto r) { read(lds + next, 0, fA, r); });
-        deal(n, Idx<kCopies>{}, [&](auto l) { copy(cur, l); });
+        deal(n, Idx<0>{}, Idx<kReads>{}, Idx<kSlots>{}, [&](auto r) { read(lds + next, 0, fA, r); });
+        deal(n, Idx<0>{}, Idx<kHalf>{}, Idx<kSlots>{}, [&](auto l) { copy(cur, l); });
         __builtin_amdgcn_sched_barrier(0);
       });
-      advance(s + kStages + 1 < nsteps);
+      last = cur;
       cur = next;
     }
     // the last copies have to land before the stores reuse LDS
