@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmxconv.so")
 ARCH = os.environ.get("MXCONV_ARCH", "gfx950")
 
 SOURCES = ["capi.cpp", "quantize.hip", "quantize_mx.hip", "conv.hip", "conv_staged.hip", "conv8.hip", "conv_mixed.hip", "conv_mx.hip",
-           "linear_capi.cpp", "linear_quant.hip", "linear_gemm.hip", "linear_fused.hip", "grad_clip.hip"]
+           "linear_capi.cpp", "linear_quant.hip", "linear_gemm.hip", "linear_few.hip", "grad_clip.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++20", "-fPIC", "-ffp-contract=off",

@@ -152,7 +152,11 @@ size_t lin_product_workspace(const LinGeom& g, LinOp op);
 hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
                               void* out, mx_dtype dtype, int64_t ld, const int32_t* offsets, void* workspace,
                               hipStream_t s);
-// Quantize-and-multiply of few tokens in one launch, where lin_fused() says so.
+// fwd and dgrad with few tokens, where lin_few() says so.
+bool lin_few(const LinGeom& g);
+hipError_t launch_lin_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, const mx_linear_qtensor* xq, void* y,
+                          mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s);
+// Quantize-and-multiply in one launch, where lin_fused() says so.
 bool lin_fused(const LinGeom& g);
 hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
                             void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s);

@@ -42,17 +42,32 @@ template <> __device__ __forceinline__ void load8<f16_t>(const f16_t* p, float* 
   for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(a[i]);
 }
 
-// A lane's 32 elements from column c of a row; zeros past the row's end and
-// where `ok` is false.  VEC: the row starts at a multiple of 16 bytes.
-template <class T, bool VEC>
-__device__ __forceinline__ void load32(const T* row, int64_t c, int64_t cols, bool ok, float* x) {
-  if (VEC && ok && c + 32 <= cols) {
+// 32 consecutive elements of a row from column c on; zeros past the row's end.
+// vec: the row starts at a multiple of 16 bytes.
+template <class T>
+__device__ __forceinline__ void load32(const T* row, int64_t c, int64_t cols, bool vec, float* x) {
+  if (vec && c + 32 <= cols) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) load8(row + c + 8 * i, x + 8 * i);
     return;
   }
+  const T* p = row + c;
+  if (c + 32 <= cols) {
+    T v[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = ok && c + i < cols ? to_f32(row[c + i]) : 0.0f;
+    for (int i = 0; i < 32; ++i) v[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = to_f32(v[i]);
+    return;
+  }
+  // the row's end: its last element where there is none, so that no load waits for a comparison
+  const int n = c < cols ? static_cast<int>(cols - c) : 0;
+  if (n == 0) p = row;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const T v = p[max(min(i, n - 1), 0)];
+    x[i] = i < n ? to_f32(v) : 0.0f;
+  }
 }
 
 __device__ __forceinline__ uint32_t amax32(const float* x) {

@@ -1,0 +1,324 @@
+// Products of the microscaled linear layers with few tokens:
+//   y[t][i] = sum_c x[t][c] w[i][c]
+// with the lines of w in a form whose columns are c (fwd: W's row form, dgrad:
+// W's column form), and x either in its row form or, for serving, unquantized
+// and quantized here (1x32 blocks), in one launch.
+//
+// Bound by w's bytes (17/32 of a byte per element), or by the launch where
+// there are few of them.  A workgroup takes SN stripes of 32 lines of w; its
+// waves take the stripes' column tiles in turn, straight from memory into the
+// MFMA's operand registers, several of them on their way, and their sums are
+// joined in LDS.  Tokens come 32 * RM at a time: from memory (L2) in the same
+// way, or quantized into LDS by the whole workgroup while the first tiles of w
+// are on their way.  Every workgroup quantizes for itself, which is cheaper
+// than a launch of its own while the tokens are few (lin_fused()).
+#include <type_traits>
+
+#include "linear.h"
+#include "linear_codes.h"
+
+namespace mx {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxWaves = 8;
+constexpr size_t kTokenLds = size_t{48} << 10;  // for a pass' codes and scales, so that three workgroups share a CU
+constexpr int kSumStride = 33;                  // words per token of a wave's sums: no bank conflicts
+
+struct FewParams {
+  const uint8_t *w, *ws;
+  int64_t kt;              // column tiles of a stripe
+  int64_t mat_stripes;     // of one expert's matrix
+  const void* x;           // unquantized tokens, or their codes
+  const uint8_t* xs;       // the codes' scales
+  int64_t ldx;
+  void* y;
+  int64_t ldy;
+  int y_dtype;
+  int vec;                 // x's rows start at multiples of 16 bytes
+  int tokens, n, k;
+  const int32_t* offsets;
+  int experts;
+  int groups;              // groups of SN stripes of one expert's matrix
+  int per_pass;            // unquantized tokens: of a pass, 32 at most
+  int units;               // workgroups with work
+  int per_xcd;
+};
+
+__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+
+// The lane's piece of what starts at p, an address that the wave has in common.
+// (The empty asm keeps the compiler from adding the lane's part first, which
+// would cost a pair of vector registers for each of these loads.)
+template <class T>
+__device__ __forceinline__ T lane_load(const uint8_t* p, int lane) {
+  asm("" : "+s"(p));
+  return ((const __attribute__((address_space(1))) T*)p)[static_cast<uint32_t>(lane)];
+}
+
+__device__ __forceinline__ void store(void* y, int dtype, int64_t i, float v) {
+  if (dtype == MX_BF16) static_cast<bf16_t*>(y)[i] = from_f32<bf16_t>(v);
+  else if (dtype == MX_F16) static_cast<f16_t*>(y)[i] = from_f32<f16_t>(v);
+  else static_cast<float*>(y)[i] = v;
+}
+
+// TX: type of the unquantized tokens, void for codes.
+template <class TX, int SN, int RM>
+__global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p) {
+  constexpr bool kFused = !std::is_void_v<TX>;
+  constexpr int kAhead = 8 / (SN * RM) > 2 ? 8 / (SN * RM) : 2;  // column tiles of a wave on their way
+  static_assert(SN * RM <= 4 && (!kFused || RM == 1));
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
+  // blocks go to the 8 XCDs in turn: XCD x takes the x-th part of the stripes,
+  // so that stripes that share scale words share an L2
+  const int i = static_cast<int>(blockIdx.x >> 3), u = static_cast<int>(blockIdx.x & 7) * p.per_xcd + i;
+  if (i >= p.per_xcd || u >= p.units) return;
+  const int e = u / p.groups, st = (u - e * p.groups) * SN;
+  int len = p.tokens;
+  int64_t row0 = 0, prow = 0;
+  if (p.experts > 0) {
+    Segment s;
+    find_segment(p.offsets, p.experts, p.tokens, e, 0, s);
+    len = __builtin_amdgcn_readfirstlane(s.len);
+    row0 = s.row0;
+    prow = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(s.prow)));
+  }
+  if (len == 0) return;
+  const int kt = static_cast<int>(p.kt);
+  const int64_t stripe = static_cast<int64_t>(e) * p.mat_stripes + st;
+  const uint8_t* wsrc = p.w + stripe * p.kt * kTileBytes;
+  const uint8_t* ssrc = p.ws + (stripe / 4) * p.kt * kScaleBytes;
+  const int sshift = 8 * static_cast<int>(stripe & 3);  // SN stripes lie in one group of four
+  const int half = lane >> 5, l32 = lane & 31;
+  const int pass = kFused ? p.per_pass : 32 * RM;
+
+  for (int t0 = 0; t0 < len; t0 += pass) {
+    const int nt = min(pass, len - t0);
+    i32x4 w[kAhead][SN], xv[kAhead][RM];
+    int ws[kAhead], xs[kAhead];
+    // the wave's column tiles; a fetch past them takes the last one again
+    const int chunk = (kt + waves - 1) / waves, begin = min(wave * chunk, kt), end = min(begin + chunk, kt);
+    auto fetch = [&](int q, int t) {
+      t = max(min(t, end - 1), 0);
+#pragma unroll
+      for (int j = 0; j < SN; ++j) w[q][j] = lane_load<i32x4>(wsrc + (j * p.kt + t) * kTileBytes, lane);
+      ws[q] = lane_load<int>(ssrc + static_cast<int64_t>(t) * kScaleBytes, lane);
+      if constexpr (!kFused) {
+        // a pass of 128 tokens may end before its last stripes, which the padding holds
+        const int64_t line = prow + t0;
+        const uint8_t* src = static_cast<const uint8_t*>(p.x) + (line / kTileR) * p.kt * kTileBytes;
+#pragma unroll
+        for (int j = 0; j < RM; ++j) xv[q][j] = lane_load<i32x4>(src + (j * p.kt + t) * kTileBytes, lane);
+        xs[q] = lane_load<int>(p.xs + ((line / kPad) * p.kt + t) * kScaleBytes, lane);
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fetch(q, begin + q);
+
+    const uint8_t* lsc = nullptr;
+    if constexpr (kFused) {
+      // a thread takes a token's 32 columns at a time; block b of token r has
+      // its codes at (b * nt + r) * 16, all scales follow
+      const int nb = kt * 2;
+      uint8_t* sc = lds + static_cast<size_t>(nb) * nt * 16;
+      lsc = sc;
+      for (int b = tid; b < nb * nt; b += threads) {
+        const int r = b / nb, c = b - r * nb;
+        const TX* src = static_cast<const TX*>(p.x) + (row0 + t0 + r) * p.ldx;
+        float v[32];
+        load32<TX>(src, static_cast<int64_t>(c) * 32, p.k, p.vec != 0, v);
+        const uint32_t code = block_code(amax32(v));
+        reinterpret_cast<uint4*>(lds)[c * nt + r] = encode32<false>(v, code, 0, 0);
+        sc[c * nt + r] = static_cast<uint8_t>(code);
+      }
+      __syncthreads();
+    }
+    f32x16 acc[RM][SN];
+#pragma unroll
+    for (int a = 0; a < RM; ++a)
+#pragma unroll
+      for (int b = 0; b < SN; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+    // lanes past the pass' tokens repeat the last one: their sums are not used
+    const int r = min(l32, nt - 1);
+    const int xshift = kFused || RM == 4 ? 0 : 8 * static_cast<int>((prow + t0) / kTileR & 3);
+    auto multiply = [&](int q, int t, bool in) {
+      int xsc;
+      if constexpr (kFused) {
+        const int b = (2 * t + half) * nt + r;
+        xv[q][0] = reinterpret_cast<const i32x4*>(lds)[b];
+        xsc = lsc[b];
+      } else {
+        xsc = static_cast<int>(static_cast<uint32_t>(xs[q]) >> xshift);
+      }
+      const int wsc = static_cast<int>(static_cast<uint32_t>(ws[q]) >> sshift);
+      const int m = in ? -1 : 0;
+      auto mul = [&](auto ac, auto bc) {
+        constexpr int A = decltype(ac)::value, B = decltype(bc)::value;
+        if constexpr (A < RM && B < SN)
+          acc[A][B] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w[q][B]), operand(xv[q][A] & m), acc[A][B], 4, 4, B, wsc, A, xsc);
+      };
+      using std::integral_constant;
+      mul(integral_constant<int, 0>{}, integral_constant<int, 0>{});
+      mul(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+      mul(integral_constant<int, 0>{}, integral_constant<int, 2>{});
+      mul(integral_constant<int, 0>{}, integral_constant<int, 3>{});
+      mul(integral_constant<int, 1>{}, integral_constant<int, 0>{});
+      mul(integral_constant<int, 2>{}, integral_constant<int, 0>{});
+      mul(integral_constant<int, 3>{}, integral_constant<int, 0>{});
+    };
+    int t = begin;
+    for (; t + kAhead < end; t += kAhead) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        multiply(q, t + q, true);
+        fetch(q, t + kAhead + q);
+      }
+    }
+    // the last ones, some of them repeated with x as zeros.  (A scale that is
+    // NaN has already made those sums NaN.)
+    if (t < end) {
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) multiply(q, min(t + q, end - 1), t + q < end);
+    }
+    // join the waves' sums in their order, 32 tokens x 32 lines at a time: a
+    // lane holds token l32, lines 8(v/4) + 4 half + v%4
+    float* sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int a = 0; a < RM; ++a) {
+      const int na = min(nt - 32 * a, 32);
+#pragma unroll
+      for (int b = 0; b < SN; ++b) {
+        __syncthreads();
+        if (l32 < na) {
+          float* d = sums + (wave * na + l32) * kSumStride + 4 * half;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) d[8 * (v / 4) + v % 4] = acc[a][b][v];
+        }
+        __syncthreads();
+        for (int j = tid; j < na * 32; j += threads) {
+          const int t = j >> 5, f = j & 31;
+          float s = 0.0f;
+          for (int q = 0; q < waves; ++q) s += sums[(q * na + t) * kSumStride + f];
+          const int col = (st + b) * 32 + f;
+          if (col < p.n) store(p.y, p.y_dtype, (row0 + t0 + 32 * a + t) * p.ldy + col, s);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Stripes of a workgroup: enough workgroups to fill the CUs first, then fewer
+// and longer ones, which share the tokens and the search for the expert.
+int stripes_per_group(int64_t stripes) { return stripes >= 2048 ? 4 : stripes >= 512 ? 2 : 1; }
+
+// Waves of a workgroup: each takes 4 column tiles at least.
+int waves_of(int64_t kt) {
+  int w = kMaxWaves;
+  while (w > 1 && kt < 4 * w) w /= 2;
+  return w;
+}
+
+// LDS of a pass: codes and scales of the tokens, and then the waves' sums in
+// their place.
+size_t fused_lds(int64_t kt, int waves, int tokens) {
+  const size_t x = static_cast<size_t>(2 * kt) * tokens * 17, s = static_cast<size_t>(waves) * (tokens < 32 ? tokens : 32) * kSumStride * 4;
+  return ((x > s ? x : s) + 15) / 16 * 16;
+}
+
+int tokens_per_pass(int64_t kt) {
+  int t = 32;
+  while (t > 0 && fused_lds(kt, waves_of(kt), t) > kTokenLds) --t;
+  return t;
+}
+
+FewParams make_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, void* y, mx_dtype y_dtype, int64_t ldy,
+                   const int32_t* offsets, int& sn) {
+  FewParams p{};
+  int64_t lines, cols;
+  const mx_form form = dgrad ? MX_FORM_COLS : MX_FORM_ROWS;
+  form_dims(g, MX_ROLE_WEIGHT, form, lines, cols);
+  p.w = static_cast<const uint8_t*>(dgrad ? wq->cols : wq->rows);
+  p.ws = dgrad ? wq->col_scales : wq->row_scales;
+  p.kt = cols / kTileC;
+  p.mat_stripes = lines / kTileR;
+  p.y = y;
+  p.ldy = ldy;
+  p.y_dtype = y_dtype;
+  p.tokens = static_cast<int>(g.m);
+  p.n = static_cast<int>(dgrad ? g.k : g.n);
+  p.k = static_cast<int>(dgrad ? g.n : g.k);
+  p.offsets = offsets;
+  p.experts = g.e;
+  const int64_t stripes = (p.n + kTileR - 1) / kTileR;
+  if (sn == 0) sn = stripes_per_group(stripes * g.ew);
+  p.groups = static_cast<int>((stripes + sn - 1) / sn);
+  p.units = p.groups * g.ew;
+  p.per_xcd = ((p.units + 7) / 8 + 3) / 4 * 4;
+  return p;
+}
+
+}  // namespace
+
+// Quantizing M tokens in every group of stripes costs about
+// M * columns * groups / 2e12 elements/s; a launch of its own costs about 4 us.
+bool lin_fused(const LinGeom& g) {
+  const int64_t kt = g.kp / kTileC, stripes = (g.n + kTileR - 1) / kTileR * g.ew;
+  const int t = tokens_per_pass(kt);
+  const int64_t groups = stripes / stripes_per_group(stripes) / g.ew + 1;
+  if (t == 0 || g.m * g.kp * groups > (int64_t{1} << 23)) return false;
+  return g.e == 0 ? g.m <= t : lin_few(g);
+}
+
+// One pass of tokens, or experts with few tokens each.
+bool lin_few(const LinGeom& g) { return g.e == 0 ? g.m <= 128 : g.m <= 16 * static_cast<int64_t>(g.e); }
+
+hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
+                            void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s) {
+  int sn = 0;
+  FewParams p = make_few(g, false, wq, y, y_dtype, ldy, offsets, sn);
+  p.x = x;
+  p.ldx = ldx;
+  const int64_t size = x_dtype == MX_F32 ? 4 : 2;
+  p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * size % 16 == 0;
+  const int waves = waves_of(p.kt), most = tokens_per_pass(p.kt);
+  p.per_pass = g.m < most ? static_cast<int>(g.m) : most;
+  const size_t lds = fused_lds(p.kt, waves, p.per_pass);
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
+  auto with = [&](auto t) {
+    using T = decltype(t);
+    sn == 4 ? go(k_lin_few<T, 4, 1>) : sn == 2 ? go(k_lin_few<T, 2, 1>) : go(k_lin_few<T, 1, 1>);
+  };
+  switch (x_dtype) {
+    case MX_BF16: with(bf16_t{}); break;
+    case MX_F16: with(f16_t{}); break;
+    default: with(float{}); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, const mx_linear_qtensor* xq, void* y,
+                          mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s) {
+  // more than one tile of tokens: all of them against one stripe
+  const bool wide = g.e == 0 && g.m > 32;
+  int sn = wide ? 1 : 0;
+  FewParams p = make_few(g, dgrad, wq, y, y_dtype, ldy, offsets, sn);
+  p.x = xq->rows;
+  p.xs = xq->row_scales;
+  const int waves = waves_of(p.kt);
+  const int64_t tokens = g.m < 32 ? g.m : 32;
+  const size_t lds = static_cast<size_t>(waves) * tokens * kSumStride * 4;
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
+  if (wide) go(k_lin_few<void, 1, 4>);
+  else sn == 4 ? go(k_lin_few<void, 4, 1>) : sn == 2 ? go(k_lin_few<void, 2, 1>) : go(k_lin_few<void, 1, 1>);
+  return hipGetLastError();
+}
+
+}  // namespace mx

@@ -446,7 +446,7 @@ Plan make_plan(const LinGeom& g, LinOp op) {
 }  // namespace
 
 size_t lin_product_workspace(const LinGeom& g, LinOp op) {
-  if (g.m == 0) return 0;
+  if (g.m == 0 || (op != LIN_WGRAD && lin_few(g))) return 0;
   const Plan pl = make_plan(g, op);
   if (pl.splits <= 1) return 0;
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
@@ -456,8 +456,9 @@ size_t lin_product_workspace(const LinGeom& g, LinOp op) {
 hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
                               void* out, mx_dtype dtype, int64_t ld, const int32_t* offsets, void* workspace,
                               hipStream_t s) {
+  if (op != LIN_WGRAD && g.m == 0) return hipSuccess;
+  if (op != LIN_WGRAD && lin_few(g)) return launch_lin_few(g, op == LIN_DGRAD, bq, aq, out, dtype, ld, offsets, s);
   const Plan pl = make_plan(g, op);
-  if (pl.units == 0) return hipSuccess;
   ProductParams p{};
   const mx_role ra = op == LIN_FWD ? MX_ROLE_ACT : MX_ROLE_GRAD, rb = op == LIN_WGRAD ? MX_ROLE_ACT : MX_ROLE_WEIGHT;
   const mx_form fa = op == LIN_WGRAD ? MX_FORM_COLS : MX_FORM_ROWS, fb = op == LIN_FWD ? MX_FORM_ROWS : MX_FORM_COLS;

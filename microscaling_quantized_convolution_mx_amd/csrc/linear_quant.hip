@@ -41,10 +41,14 @@ struct QuantParams {
   uint64_t seed;
 };
 
+constexpr int kStageRow = kTileC + 1;  // words between rows in LDS: lanes 32 rows apart hit different banks
+
+// VEC: rows start at multiples of 16 bytes.
 template <class T, bool SQUARE, bool SR, bool VEC>
 __global__ __launch_bounds__(256) void k_lin_quantize(const QuantParams p) {
   __shared__ __attribute__((aligned(16))) uint8_t tiles[4][2][kTileBytes];
   __shared__ __attribute__((aligned(16))) uint8_t rsc[2][kScaleBytes], csc[2][kScaleBytes];
+  __shared__ float stage[VEC ? 1 : 4][VEC ? 1 : 32 * kStageRow];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // the workgroup's 128 rows: source row and count, padded row, and the
   // matrix' base in the column form
@@ -71,15 +75,40 @@ __global__ __launch_bounds__(256) void k_lin_quantize(const QuantParams p) {
     left = p.rows - pb;
   }
   const int r = lane & 31, half = lane >> 5;
-  const bool ok = 32 * wave + r < left;
   const int64_t row = row0 + 32 * wave + r;
-  const T* src = static_cast<const T*>(p.src) + row * p.ld;
+  const T* src = static_cast<const T*>(p.src) + (row0 + 32 * wave) * p.ld;
+  const int nr = static_cast<int>(min<int64_t>(left - 32 * wave, 32));  // rows of the wave, if any
   const int64_t ct0 = static_cast<int64_t>(bx) * 2;  // first column tile
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int64_t c = (ct0 + t) * kTileC + 32 * half;
     float x[32];
-    load32<T, VEC>(src, c, p.cols, ok, x);
+    if constexpr (VEC) {
+      if (r < nr && c < p.cols) {
+        load32(src + r * p.ld, c, p.cols, true, x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+      }
+    } else {
+      // a lane of its own for each column, so that a load takes one piece of a
+      // row; through LDS to the lane that encodes it
+      float* ls = stage[wave];
+      const int64_t lc = (ct0 + t) * kTileC + lane;
+      const bool in = lc < p.cols && nr > 0;
+      const T* col = src + (in ? lc : 0);
+      T v[32];
+      if (nr > 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = col[min(i, nr - 1) * p.ld];
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ls[i * kStageRow + lane] = in && i < nr ? to_f32(v[i]) : 0.0f;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = ls[r * kStageRow + 32 * half + i];
+      __builtin_amdgcn_wave_barrier();
+    }
     uint32_t m = amax32(x);
     if constexpr (SQUARE) {
 #pragma unroll
@@ -131,8 +160,8 @@ __device__ __forceinline__ float scale_value(uint32_t code) {
   return code == 0xFFu ? __uint_as_float(0x7FC00000u) : (code == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(code << 23));
 }
 
-// Workgroups as in the quantizer; a lane decodes its 16 bytes.  COLS: the
-// lane's 32 values are a column of the matrix.
+// Workgroups as in the quantizer.  COLS: from the column form, where a lane's
+// 16 bytes are a column of the matrix.
 template <class T, bool COLS, bool VEC>
 __global__ __launch_bounds__(256) void k_lin_dequantize(const QuantParams p, T* __restrict__ dst) {
   using F = Fmt<FMT_E2M1>;
@@ -156,48 +185,54 @@ __global__ __launch_bounds__(256) void k_lin_dequantize(const QuantParams p, T* 
     crow0 = e * p.cmat;
   }
   const int64_t ct0 = static_cast<int64_t>(bx) * 2;
-  const int r = lane & 31, half = lane >> 5;
+  auto value = [](uint32_t c, float scale) {
+    const float v = code_value<F>(c & 7u) * scale;
+    return from_f32<T>((c & 8u) ? -v : v);
+  };
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    uint4 w;
-    uint32_t code;
     if constexpr (!COLS) {
-      w = reinterpret_cast<const uint4*>(p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes)[lane];
-      code = p.rscales[((prow / kPad) * p.rkt + ct0 + t) * kScaleBytes + lane * 4 + wave];
-    } else {
-      const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
-      const int64_t pr = pr0 + 32 * wave;
-      w = *reinterpret_cast<const uint4*>(p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16);
-      code = p.cscales[((stripe / 4) * p.ckt + pr / kTileC) * kScaleBytes + (((pr / 32) & 1) * 32 + r) * 4 + (stripe & 3)];
-    }
-    const float scale = scale_value(code);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    T y[32];
+      // N elements, 16 bytes where rows allow, per lane and pass, so that a
+      // store takes whole pieces of rows
+      constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
+      constexpr int P = kTileC / N;
+      const uint8_t* tile = p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes;
+      const uint8_t* sc = p.rscales + ((prow / kPad) * p.rkt + ct0 + t) * kScaleBytes + wave;
+#pragma unroll 8
+      for (int s = 0; s < kTileR * P / 64; ++s) {
+        const int r = (s * 64 + lane) / P, j = (s * 64 + lane) % P * N, half = j >> 5;
+        const uint8_t* at = tile + half * 512 + r * 16 + (j & 31) / 2;
+        uint32_t w;
+        if constexpr (N == 8) w = *reinterpret_cast<const uint32_t*>(at);
+        else if constexpr (N == 4) w = *reinterpret_cast<const uint16_t*>(at);
+        else w = *at >> (4 * (j & 1));
+        const float scale = scale_value(sc[(half * 32 + r) * 4]);
+        struct alignas(N * sizeof(T)) { T e[N]; } y;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t c = (ww[i >> 3] >> (4 * (i & 7))) & 0xFu;
-      const float v = code_value<F>(c & 7u) * scale;
-      y[i] = from_f32<T>((c >> 3) ? -v : v);
-    }
-    if constexpr (!COLS) {
-      const int64_t c = (ct0 + t) * kTileC + 32 * half;
-      if (32 * wave + r >= left) continue;
-      T* d = dst + (row0 + 32 * wave + r) * p.ld + c;
-      if (VEC && c + 32 <= p.cols) {
+        for (int i = 0; i < N; ++i) y.e[i] = value(w >> (4 * i), scale);
+        const int64_t c = (ct0 + t) * kTileC + j;
+        if (32 * wave + r >= left) continue;
+        T* d = dst + (row0 + 32 * wave + r) * p.ld + c;
+        if (c + N <= p.cols) {
+          *reinterpret_cast<decltype(y)*>(d) = y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(32 * sizeof(T) / 16); ++i)
-          reinterpret_cast<uint4*>(d)[i] = reinterpret_cast<const uint4*>(y)[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < p.cols) d[i] = y[i];
+          for (int i = 0; i < N; ++i)
+            if (c + i < p.cols) d[i] = y.e[i];
+        }
       }
     } else {
+      const int r = lane & 31, half = lane >> 5;
+      const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
+      const int64_t pr = pr0 + 32 * wave;
+      const uint4 w = *reinterpret_cast<const uint4*>(p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16);
+      const float scale = scale_value(p.cscales[((stripe / 4) * p.ckt + pr / kTileC) * kScaleBytes + (((pr / 32) & 1) * 32 + r) * 4 + (stripe & 3)]);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
       const int64_t c = (ct0 + t) * kTileC + 32 * half + r;
       if (c >= p.cols) continue;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (32 * wave + i < left) dst[(row0 + 32 * wave + i) * p.ld + c] = y[i];
+        if (32 * wave + i < left) dst[(row0 + 32 * wave + i) * p.ld + c] = value(ww[i >> 3] >> (4 * (i & 7)), scale);
     }
   }
 }
