@@ -8,8 +8,7 @@
 // there are few of them.  A workgroup takes SN stripes of 32 lines of w; its
 // waves take the stripes' column tiles in turn, straight from memory into the
 // MFMA's operand registers, several of them on their way, and their sums are
-// joined in LDS.  Tokens come 32 * RM at a time: from memory (L2) in the same
-// way, or quantized into LDS by the whole workgroup while the first tiles of w
+// joined in LDS.  Tokens come 32 at a time: from memory (L2) in the same way, or quantized into LDS by the whole workgroup while the first tiles of w
 // are on their way.  Every workgroup quantizes for itself, which is cheaper
 // than a launch of its own while the tokens are few (lin_fused()).
 #include <type_traits>
@@ -66,11 +65,10 @@ __device__ __forceinline__ void store(void* y, int dtype, int64_t i, float v) {
 }
 
 // TX: type of the unquantized tokens, void for codes.
-template <class TX, int SN, int RM>
+template <class TX, int SN>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p) {
   constexpr bool kFused = !std::is_void_v<TX>;
-  constexpr int kAhead = 8 / (SN * RM) > 2 ? 8 / (SN * RM) : 2;  // column tiles of a wave on their way
-  static_assert(SN * RM <= 4 && (!kFused || RM == 1));
+  constexpr int kAhead = 8 / SN;  // column tiles of a wave on their way
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
@@ -95,11 +93,11 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
   const uint8_t* ssrc = p.ws + (stripe / 4) * p.kt * kScaleBytes;
   const int sshift = 8 * static_cast<int>(stripe & 3);  // SN stripes lie in one group of four
   const int half = lane >> 5, l32 = lane & 31;
-  const int pass = kFused ? p.per_pass : 32 * RM;
+  const int pass = kFused ? p.per_pass : 32;
 
   for (int t0 = 0; t0 < len; t0 += pass) {
     const int nt = min(pass, len - t0);
-    i32x4 w[kAhead][SN], xv[kAhead][RM];
+    i32x4 w[kAhead][SN], xv[kAhead];
     int ws[kAhead], xs[kAhead];
     // the wave's column tiles; a fetch past them takes the last one again
     const int chunk = (kt + waves - 1) / waves, begin = min(wave * chunk, kt), end = min(begin + chunk, kt);
@@ -109,11 +107,8 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
       for (int j = 0; j < SN; ++j) w[q][j] = lane_load<i32x4>(wsrc + (j * p.kt + t) * kTileBytes, lane);
       ws[q] = lane_load<int>(ssrc + static_cast<int64_t>(t) * kScaleBytes, lane);
       if constexpr (!kFused) {
-        // a pass of 128 tokens may end before its last stripes, which the padding holds
         const int64_t line = prow + t0;
-        const uint8_t* src = static_cast<const uint8_t*>(p.x) + (line / kTileR) * p.kt * kTileBytes;
-#pragma unroll
-        for (int j = 0; j < RM; ++j) xv[q][j] = lane_load<i32x4>(src + (j * p.kt + t) * kTileBytes, lane);
+        xv[q] = lane_load<i32x4>(static_cast<const uint8_t*>(p.x) + ((line / kTileR) * p.kt + t) * kTileBytes, lane);
         xs[q] = lane_load<int>(p.xs + ((line / kPad) * p.kt + t) * kScaleBytes, lane);
       }
     };
@@ -138,40 +133,34 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
       }
       __syncthreads();
     }
-    f32x16 acc[RM][SN];
+    f32x16 acc[SN];
 #pragma unroll
-    for (int a = 0; a < RM; ++a)
+    for (int j = 0; j < SN; ++j)
 #pragma unroll
-      for (int b = 0; b < SN; ++b)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[a][b][v] = 0.0f;
+      for (int v = 0; v < 16; ++v) acc[j][v] = 0.0f;
     // lanes past the pass' tokens repeat the last one: their sums are not used
     const int r = min(l32, nt - 1);
-    const int xshift = kFused || RM == 4 ? 0 : 8 * static_cast<int>((prow + t0) / kTileR & 3);
+    const int xshift = kFused ? 0 : 8 * static_cast<int>((prow + t0) / kTileR & 3);
     auto multiply = [&](int q, int t, bool in) {
       int xsc;
       if constexpr (kFused) {
         const int b = (2 * t + half) * nt + r;
-        xv[q][0] = reinterpret_cast<const i32x4*>(lds)[b];
+        xv[q] = reinterpret_cast<const i32x4*>(lds)[b];
         xsc = lsc[b];
       } else {
         xsc = static_cast<int>(static_cast<uint32_t>(xs[q]) >> xshift);
       }
       const int wsc = static_cast<int>(static_cast<uint32_t>(ws[q]) >> sshift);
       const int m = in ? -1 : 0;
-      auto mul = [&](auto ac, auto bc) {
-        constexpr int A = decltype(ac)::value, B = decltype(bc)::value;
-        if constexpr (A < RM && B < SN)
-          acc[A][B] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w[q][B]), operand(xv[q][A] & m), acc[A][B], 4, 4, B, wsc, A, xsc);
+      auto mul = [&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+        if constexpr (J < SN)
+          acc[J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w[q][J]), operand(xv[q] & m), acc[J], 4, 4, J, wsc, 0, xsc);
       };
-      using std::integral_constant;
-      mul(integral_constant<int, 0>{}, integral_constant<int, 0>{});
-      mul(integral_constant<int, 0>{}, integral_constant<int, 1>{});
-      mul(integral_constant<int, 0>{}, integral_constant<int, 2>{});
-      mul(integral_constant<int, 0>{}, integral_constant<int, 3>{});
-      mul(integral_constant<int, 1>{}, integral_constant<int, 0>{});
-      mul(integral_constant<int, 2>{}, integral_constant<int, 0>{});
-      mul(integral_constant<int, 3>{}, integral_constant<int, 0>{});
+      mul(std::integral_constant<int, 0>{});
+      mul(std::integral_constant<int, 1>{});
+      mul(std::integral_constant<int, 2>{});
+      mul(std::integral_constant<int, 3>{});
     };
     int t = begin;
     for (; t + kAhead < end; t += kAhead) {
@@ -191,24 +180,20 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
     // lane holds token l32, lines 8(v/4) + 4 half + v%4
     float* sums = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int a = 0; a < RM; ++a) {
-      const int na = min(nt - 32 * a, 32);
+    for (int j = 0; j < SN; ++j) {
+      __syncthreads();
+      if (l32 < nt) {
+        float* d = sums + (wave * nt + l32) * kSumStride + 4 * half;
 #pragma unroll
-      for (int b = 0; b < SN; ++b) {
-        __syncthreads();
-        if (l32 < na) {
-          float* d = sums + (wave * na + l32) * kSumStride + 4 * half;
-#pragma unroll
-          for (int v = 0; v < 16; ++v) d[8 * (v / 4) + v % 4] = acc[a][b][v];
-        }
-        __syncthreads();
-        for (int j = tid; j < na * 32; j += threads) {
-          const int t = j >> 5, f = j & 31;
-          float s = 0.0f;
-          for (int q = 0; q < waves; ++q) s += sums[(q * na + t) * kSumStride + f];
-          const int col = (st + b) * 32 + f;
-          if (col < p.n) store(p.y, p.y_dtype, (row0 + t0 + 32 * a + t) * p.ldy + col, s);
-        }
+        for (int v = 0; v < 16; ++v) d[8 * (v / 4) + v % 4] = acc[j][v];
+      }
+      __syncthreads();
+      for (int i = tid; i < nt * 32; i += threads) {
+        const int t = i >> 5, f = i & 31;
+        float s = 0.0f;
+        for (int q = 0; q < waves; ++q) s += sums[(q * nt + t) * kSumStride + f];
+        const int col = (st + j) * 32 + f;
+        if (col < p.n) store(p.y, p.y_dtype, (row0 + t0 + t) * p.ldy + col, s);
       }
     }
     __syncthreads();
@@ -229,7 +214,7 @@ int waves_of(int64_t kt) {
 // LDS of a pass: codes and scales of the tokens, and then the waves' sums in
 // their place.
 size_t fused_lds(int64_t kt, int waves, int tokens) {
-  const size_t x = static_cast<size_t>(2 * kt) * tokens * 17, s = static_cast<size_t>(waves) * (tokens < 32 ? tokens : 32) * kSumStride * 4;
+  const size_t x = static_cast<size_t>(2 * kt) * tokens * 17, s = static_cast<size_t>(waves) * tokens * kSumStride * 4;
   return ((x > s ? x : s) + 15) / 16 * 16;
 }
 
@@ -258,7 +243,7 @@ FewParams make_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, vo
   p.offsets = offsets;
   p.experts = g.e;
   const int64_t stripes = (p.n + kTileR - 1) / kTileR;
-  if (sn == 0) sn = stripes_per_group(stripes * g.ew);
+  sn = stripes_per_group(stripes * g.ew);
   p.groups = static_cast<int>((stripes + sn - 1) / sn);
   p.units = p.groups * g.ew;
   p.per_xcd = ((p.units + 7) / 8 + 3) / 4 * 4;
@@ -277,12 +262,14 @@ bool lin_fused(const LinGeom& g) {
   return g.e == 0 ? g.m <= t : lin_few(g);
 }
 
-// One pass of tokens, or experts with few tokens each.
-bool lin_few(const LinGeom& g) { return g.e == 0 ? g.m <= 128 : g.m <= 16 * static_cast<int64_t>(g.e); }
+// Two passes of tokens, or experts with few tokens each.  (64x4096x4096 takes
+// 7.7 us here and 11.6 in 128x128 tiles, 64x1024x1024 6.7 and 6.3; a third
+// pass, 96x4096x4096 10.3 and 11.7, 96x1024x1024 8.9 and 6.3.)
+bool lin_few(const LinGeom& g) { return g.e == 0 ? g.m <= 64 : g.m <= 16 * static_cast<int64_t>(g.e); }
 
 hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
                             void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s) {
-  int sn = 0;
+  int sn;
   FewParams p = make_few(g, false, wq, y, y_dtype, ldy, offsets, sn);
   p.x = x;
   p.ldx = ldx;
@@ -294,7 +281,7 @@ hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
   auto with = [&](auto t) {
     using T = decltype(t);
-    sn == 4 ? go(k_lin_few<T, 4, 1>) : sn == 2 ? go(k_lin_few<T, 2, 1>) : go(k_lin_few<T, 1, 1>);
+    sn == 4 ? go(k_lin_few<T, 4>) : sn == 2 ? go(k_lin_few<T, 2>) : go(k_lin_few<T, 1>);
   };
   switch (x_dtype) {
     case MX_BF16: with(bf16_t{}); break;
@@ -306,9 +293,7 @@ hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const
 
 hipError_t launch_lin_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, const mx_linear_qtensor* xq, void* y,
                           mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s) {
-  // more than one tile of tokens: all of them against one stripe
-  const bool wide = g.e == 0 && g.m > 32;
-  int sn = wide ? 1 : 0;
+  int sn;
   FewParams p = make_few(g, dgrad, wq, y, y_dtype, ldy, offsets, sn);
   p.x = xq->rows;
   p.xs = xq->row_scales;
@@ -316,8 +301,7 @@ hipError_t launch_lin_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor*
   const int64_t tokens = g.m < 32 ? g.m : 32;
   const size_t lds = static_cast<size_t>(waves) * tokens * kSumStride * 4;
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
-  if (wide) go(k_lin_few<void, 1, 4>);
-  else sn == 4 ? go(k_lin_few<void, 4, 1>) : sn == 2 ? go(k_lin_few<void, 2, 1>) : go(k_lin_few<void, 1, 1>);
+  sn == 4 ? go(k_lin_few<void, 4>) : sn == 2 ? go(k_lin_few<void, 2>) : go(k_lin_few<void, 1>);
   return hipGetLastError();
 }
 

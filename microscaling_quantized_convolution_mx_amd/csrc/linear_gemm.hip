@@ -57,32 +57,41 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// Output tile, waves and LDS stages of a workgroup.
+template <int M, int N, int A, int B, int S>
+struct Shape {
+  static constexpr int TM = M, TN = N, WM = A, WN = B, kStages = S;
+  static constexpr int kThreads = 64 * A * B;
+};
+using Big = Shape<256, 256, 2, 2, 4>;
+using Small = Shape<128, 128, 2, 2, 4>;
+
 // LDS that a wave's stores go through: 32 rows of its outputs, 16 bytes apart
 // from each other so that neither the writes nor the reads conflict.
-template <class U, int RM>
-__host__ __device__ constexpr int store_bytes() { return 32 * (RM * 32 * static_cast<int>(sizeof(U)) + 16); }
+template <class U, int RN>
+__host__ __device__ constexpr int store_bytes() { return 32 * (RN * 32 * static_cast<int>(sizeof(U)) + 16); }
 
-// Stores the wave's RM x RM results.  The MFMA leaves lane l with row l%32
+// Stores the wave's RM x RN results of 32x32.  The MFMA leaves lane l with row l%32
 // and 4 columns each at 8v + 4(l/32), v = 0..3: stored from there, a memory
 // instruction would write 32 short pieces.  Through LDS, 32 rows at a time,
 // it writes whole rows, 16 bytes per lane.
 // dst: the tile's first output; rleft, cleft: rows and columns from there on
 // that exist; vec: rows start at multiples of 16 bytes.
-template <int RM, class U>
-__device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RM], uint8_t* buf, U* dst, int64_t ld, bool vec, int64_t rleft,
+template <int RM, int RN, class U>
+__device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t* buf, U* dst, int64_t ld, bool vec, int64_t rleft,
                                            int64_t cleft, int lane, int wm, int wn) {
-  constexpr int W = RM * 32;                                  // columns of the wave
+  constexpr int W = RN * 32;                                  // columns of the wave
   constexpr int kRow = W * static_cast<int>(sizeof(U)) + 16;  // bytes between rows in LDS
   constexpr int N = 16 / static_cast<int>(sizeof(U));         // elements of 16 bytes
   constexpr int P = W / N;                                    // 16-byte pieces of a row
   const int64_t c0 = wn * W;
   cleft -= c0;
-  rleft -= wm * W;
-  dst += static_cast<int64_t>(wm * W) * ld + c0;
+  rleft -= wm * RM * 32;
+  dst += static_cast<int64_t>(wm * RM * 32) * ld + c0;
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
 #pragma unroll
-    for (int j = 0; j < RM; ++j)
+    for (int j = 0; j < RN; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         struct alignas(4 * sizeof(U)) { U e[4]; } q;
@@ -144,24 +153,24 @@ __device__ __forceinline__ void wait_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// TILE x TILE outputs per workgroup, 4 waves of TILE/2 x TILE/2 in MFMAs of
-// 32x32x64.  One step contracts 128 columns: two MFMA slices.  A tile in LDS
-// is read as it is, 64 lanes x 16 consecutive bytes, which is free of bank
-// conflicts.
-template <class T, int TILE, bool CONTRACT>
-__global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
-  constexpr int RM = TILE / 64;               // MFMA rows and columns of a wave
-  constexpr int NQ = TILE / 64;               // tiles a wave copies per operand and step
-  constexpr int kOpnd = (TILE / 32) * kStepTiles * kTileBytes;
-  constexpr int kOpndS = (TILE / 128) * kStepTiles * kScaleBytes;
-  constexpr int NS = TILE / 128;              // 256-byte groups of scales a wave copies per step
-  constexpr int kStage = 2 * kOpnd + 2 * kOpndS;
-  constexpr int kStages = 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage];
+// TM x TN outputs per workgroup, by WM x WN waves in MFMAs of 32x32x64.  One
+// step contracts 128 columns: two MFMA slices.  A tile in LDS is read as it
+// is, 64 lanes x 16 consecutive bytes, which is free of bank conflicts.
+template <class T, class Shape, bool CONTRACT>
+__global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(const ProductParams p) {
+  constexpr int TM = Shape::TM, TN = Shape::TN, WM = Shape::WM, WN = Shape::WN, kStages = Shape::kStages;
+  constexpr int RM = TM / WM / 32, RN = TN / WN / 32;  // MFMA rows and columns of a wave
+  constexpr int kWaves = WM * WN;
+  constexpr int kOpndA = TM / 32 * kStepTiles * kTileBytes, kOpndB = TN / 32 * kStepTiles * kTileBytes;
+  constexpr int kGroupsA = TM / kPad * kStepTiles, kGroups = (TM + TN) / kPad * kStepTiles;  // 256-byte groups of scales
+  constexpr int kScales = kOpndA + kOpndB;                                                  // their place in a stage
+  constexpr int kStage = kScales + kGroups * kScaleBytes;
+  constexpr int kStoreBytes = kWaves * store_bytes<T, RN>();
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage > kStoreBytes ? kStages * kStage : kStoreBytes];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % WM, wn = wave / WM;
 
   // Work: (expert, row tile, column tile, split).  Blocks go to the 8 XCDs in
   // turn; XCD x takes the x-th eighth of the work, so that what its blocks
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     else {
       Segment s;
       int ti_all = 0;
-      find_segment(p.offsets, p.experts, p.tokens, -1, TILE, s, &ti_all);
+      find_segment(p.offsets, p.experts, p.tokens, -1, TM, s, &ti_all);
       total = static_cast<int64_t>(ti_all) * p.tiles_j;
     }
     const int64_t per = (total + 7) / 8;
@@ -203,7 +212,7 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     ti = bi * G + r % h;
     tj = r / h;
     if constexpr (CONTRACT) {
-      arow = static_cast<int64_t>(ti) * TILE;
+      arow = static_cast<int64_t>(ti) * TM;
       orow = arow;
       rleft = p.rows - orow;
       if (p.experts > 0) {
@@ -216,24 +225,24 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
         ksteps = p.ktiles / kStepTiles;
         sp = z;
       }
-      brow = static_cast<int64_t>(tj) * TILE;
+      brow = static_cast<int64_t>(tj) * TN;
     } else {
       ksteps = p.ktiles / kStepTiles;
       if (p.experts > 0) {
         Segment s;
-        find_segment(p.offsets, p.experts, p.tokens, ti, TILE, s);
-        arow = s.prow + static_cast<int64_t>(s.unit) * TILE;
-        orow = s.row0 + static_cast<int64_t>(s.unit) * TILE;
-        rleft = s.len - static_cast<int64_t>(s.unit) * TILE;
+        find_segment(p.offsets, p.experts, p.tokens, ti, TM, s);
+        arow = s.prow + static_cast<int64_t>(s.unit) * TM;
+        orow = s.row0 + static_cast<int64_t>(s.unit) * TM;
+        rleft = s.len - static_cast<int64_t>(s.unit) * TM;
         brow = s.e * p.bmat;
       } else {
         sp = z;
-        arow = orow = static_cast<int64_t>(ti) * TILE;
+        arow = orow = static_cast<int64_t>(ti) * TM;
         rleft = p.rows - orow;
       }
-      brow += static_cast<int64_t>(tj) * TILE;
+      brow += static_cast<int64_t>(tj) * TN;
     }
-    cleft = p.cols - static_cast<int64_t>(tj) * TILE;
+    cleft = p.cols - static_cast<int64_t>(tj) * TN;
   }
   int s_begin = 0, nsteps = ksteps;
   if (p.splits > 1) {
@@ -251,96 +260,95 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
   nsteps = __builtin_amdgcn_readfirstlane(nsteps);
 
   // Copies.  A step's tiles go from memory to LDS as they are stored, without
-  // passing registers: wave w's copy q takes tile w%2 of stripe 2q + w/2 of
-  // an operand, 64 lanes x 16 bytes, and one of the scales' 256-byte groups
-  // (for 256 rows of an operand one of a, one of b; for 128 rows the waves
-  // take a's two and b's two).  A stripe past the operand's end is read as
-  // its last one: those outputs are not stored.
-  const uint8_t *asrc[NQ], *bsrc[NQ], *ssrc[NS];
-  uint32_t sdst[NS];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int64_t st = 2 * q + (wave >> 1);
-    const int64_t sa = min(arow / kTileR + st, p.a_rows / kTileR - 1), sb = min(brow / kTileR + st, p.b_rows / kTileR - 1);
-    asrc[q] = p.a + (sa * p.akt + k0 + (wave & 1)) * kTileBytes;
-    bsrc[q] = p.b + (sb * p.bkt + k0 + (wave & 1)) * kTileBytes;
-  }
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const bool of_b = NS == 2 ? i == 1 : (wave >> 1) == 1;
-    const int64_t g = NS == 2 ? wave >> 1 : 0;  // 128 rows of the tile
-    const int64_t r = min((of_b ? brow : arow) / kPad + g, (of_b ? p.b_rows : p.a_rows) / kPad - 1);
-    ssrc[i] = (of_b ? p.bs : p.as) + (r * (of_b ? p.bkt : p.akt) + k0 + (wave & 1)) * kScaleBytes;
-    sdst[i] = 2 * kOpnd + (of_b ? kOpndS : 0) + static_cast<uint32_t>(g * kStepTiles + (wave & 1)) * kScaleBytes;
-  }
+  // passing registers: copy l of wave w takes tile l * kWaves + w of a's, then
+  // b's tiles (two columns of them, 64 lanes x 16 bytes each) and then groups
+  // of scales.  A stripe past the operand's end is read as its last one:
+  // those outputs are not stored.
+  constexpr int kTilesA = TM / 16 / kWaves, kTiles = (TM + TN) / 16 / kWaves;
+  constexpr int kScaleCopies = (kGroups + kWaves - 1) / kWaves, kCopies = kTiles + kScaleCopies;
+  static_assert(TM / 16 % kWaves == 0 && TN / 16 % kWaves == 0);
+  const uint8_t *src[kTiles], *ssrc[kScaleCopies];
+  uint32_t sdst[kScaleCopies];
+  static_for<kTiles>([&](auto lc) {
+    constexpr int L = decltype(lc)::value;
+    constexpr bool of_b = L >= kTilesA;
+    const int i = (of_b ? L - kTilesA : L) * kWaves + wave;
+    const int64_t st = min((of_b ? brow : arow) / kTileR + i / kStepTiles, (of_b ? p.b_rows : p.a_rows) / kTileR - 1);
+    src[L] = (of_b ? p.b : p.a) + (st * (of_b ? p.bkt : p.akt) + k0 + i % kStepTiles) * kTileBytes;
+  });
+  static_for<kScaleCopies>([&](auto lc) {
+    constexpr int L = decltype(lc)::value;
+    const int i = min(L * kWaves + wave, kGroups - 1);  // (the last group may be copied twice)
+    const bool of_b = i >= kGroupsA;
+    const int j = of_b ? i - kGroupsA : i;
+    const int64_t g = min((of_b ? brow : arow) / kPad + j / kStepTiles, (of_b ? p.b_rows : p.a_rows) / kPad - 1);
+    ssrc[L] = (of_b ? p.bs : p.as) + (g * (of_b ? p.bkt : p.akt) + k0 + j % kStepTiles) * kScaleBytes;
+    sdst[L] = kScales + static_cast<uint32_t>(i) * kScaleBytes;
+  });
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
   // copy l of the step that the sources stand at, into the stage at `to`
-  constexpr int kCopies = 2 * NQ + NS;
   auto copy = [&](uint32_t to, auto l) {
     constexpr int L = decltype(l)::value;
-    if constexpr (L < 2 * NQ) {
-      copy_lds<16>(L % 2 ? bsrc[L / 2] : asrc[L / 2], lds0 + to + (L % 2 ? kOpnd : 0) + (L / 2) * 4096 + wave * kTileBytes, lane);
-    } else {
-      copy_lds<4>(ssrc[L - 2 * NQ], lds0 + to + sdst[L - 2 * NQ], lane);
-    }
+    if constexpr (L < kTiles) copy_lds<16>(src[L], lds0 + to + (L * kWaves + wave) * kTileBytes, lane);
+    else copy_lds<4>(ssrc[L - kTiles], lds0 + to + sdst[L - kTiles], lane);
   };
   auto advance = [&](bool on) {
     const int d = on ? 1 : 0;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      asrc[q] += d * (kStepTiles * kTileBytes);
-      bsrc[q] += d * (kStepTiles * kTileBytes);
-    }
+    for (int q = 0; q < kTiles; ++q) src[q] += d * (kStepTiles * kTileBytes);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) ssrc[i] += d * (kStepTiles * kScaleBytes);
+    for (int i = 0; i < kScaleCopies; ++i) ssrc[i] += d * (kStepTiles * kScaleBytes);
   };
 
-  f32x16 acc[RM][RM];
+  f32x16 acc[RM][RN];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int j = 0; j < RM; ++j)
+    for (int j = 0; j < RN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
   struct Frags {
-    i32x8 a[RM], b[RM];
+    i32x8 a[RM], b[RN];
     int sa, sb;
   };
   Frags fA, fB;
+  // a wave's scales: the bytes of its 1, 2 or 4 stripes among 128 rows' four
+  auto read_scales = [&](const uint8_t* s, int stripe, int n, int j) -> int {
+    const uint8_t* at = s + ((stripe >> 2) * kStepTiles + j) * kScaleBytes + 4 * lane + (stripe & 3);
+    return n == 4 ? *reinterpret_cast<const int*>(at) : n == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
+  };
   // read r of slice j: the scales, then the tiles in the order of their use
-  constexpr int kReads = 2 * RM + 2;
+  constexpr int kReads = RM + RN + 2;
   auto read = [&](const uint8_t* st, int j, Frags& f, auto r) {
     constexpr int R = decltype(r)::value;
-    if constexpr (R < 2) {
-      // a wave of 64 rows uses two bytes of its 128 rows' scales
-      const uint8_t* s = st + 2 * kOpnd + R * kOpndS;
-      const int w = R ? wn : wm;
-      (R ? f.sb : f.sa) = RM == 4 ? reinterpret_cast<const int*>(s + (w * kStepTiles + j) * kScaleBytes)[lane]
-                                  : reinterpret_cast<const uint16_t*>(s + j * kScaleBytes)[2 * lane + w];
-    } else if constexpr (R == 2 || R >= RM + 3) {
-      constexpr int I = R == 2 ? 0 : R - RM - 2;
+    if constexpr (R == 0) {
+      f.sa = read_scales(st + kScales, wm * RM, RM, j);
+    } else if constexpr (R == 1) {
+      f.sb = read_scales(st + kScales + kGroupsA * kScaleBytes, wn * RN, RN, j);
+    } else if constexpr (R == 2 || R >= RN + 3) {
+      constexpr int I = R == 2 ? 0 : R - RN - 2;
       f.a[I] = operand(reinterpret_cast<const i32x4*>(st + ((wm * RM + I) * kStepTiles + j) * kTileBytes)[lane]);
     } else {
       constexpr int I = R - 3;
-      f.b[I] = operand(reinterpret_cast<const i32x4*>(st + kOpnd + ((wn * RM + I) * kStepTiles + j) * kTileBytes)[lane]);
+      f.b[I] = operand(reinterpret_cast<const i32x4*>(st + kOpndA + ((wn * RN + I) * kStepTiles + j) * kTileBytes)[lane]);
     }
   };
 
-  // Step s, on stage s%4, with slice 0's operands read during step s-1:
+  // Step s, on stage s%S of S, with slice 0's operands read during step s-1:
   //   multiply slice 0, reading slice 1 and copying the second half of step
-  //   s+3 into stage (s+3)%4;
-  //   barrier: every wave has read all of stage s%4, and its copies of step
-  //   s+1 have arrived (those of steps s+2 and s+3 may be on their way);
+  //   s+S-1 into stage (s+S-1)%S;
+  //   barrier: every wave has read all of stage s%S, and its copies of step
+  //   s+1 have arrived (those of the S-2 steps after may be on their way);
   //   multiply slice 1, reading slice 0 of step s+1 and copying the first
-  //   half of step s+4 into stage s%4.
+  //   half of step s+S into stage s%S.
   // With one wave per SIMD nothing else hides an LDS access, so reads and
   // copies are dealt out between the MFMAs: an MFMA lasts 32 cycles, in which
   // LDS serves about one 1 KiB access of each of the four waves.  Copies past
   // the last step repeat it, into stages that nothing reads.
-  constexpr int kSlots = RM * RM;
+  constexpr int kSlots = RM * RN;
   auto mfma = [&](const Frags& f, auto n) {
-    constexpr int I = decltype(n)::value / RM, J = decltype(n)::value % RM;
+    constexpr int I = decltype(n)::value / RN, J = decltype(n)::value % RN;
     acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f.b[J], f.a[I], acc[I][J], 4, 4, J, f.sb, I, f.sa);
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -388,8 +396,8 @@ __global__ __launch_bounds__(256) void k_lin_product(const ProductParams p) {
     wait_barrier<0>();
   }
 
-  store_wave<RM>(acc, lds + wave * store_bytes<T, RM>(), out + orow * p.ld + static_cast<int64_t>(tj) * TILE, p.ld, p.vec != 0, rleft, cleft,
-                 lane, wm, wn);
+  store_wave<RM, RN>(acc, lds + wave * store_bytes<T, RN>(), out + orow * p.ld + static_cast<int64_t>(tj) * TN, p.ld, p.vec != 0, rleft,
+                     cleft, lane, wm, wn);
 }
 
 // Sums the pieces of a split product in their order, 4 columns per thread.
@@ -408,39 +416,56 @@ __global__ __launch_bounds__(256) void k_lin_reduce(const float* __restrict__ pa
 }
 
 struct Plan {
-  int tile;     // 128 or 256
+  bool big;     // Big or Small tiles
   int64_t tiles_i, tiles_j;
   int splits, split_steps;
   int64_t units;  // workgroups, at most
 };
 
+// Tiles and split by estimated time, in us, fitted to measured products (bf16
+// outputs, 2048^3 to 8192^3 and 128..2048 rows of 1024..8192 columns):
+//   Big    a round of 256 workgroups takes 0.8 per step and 9 for its first
+//          loads and its stores (4096x4096x4096: 39)
+//   Small  a round of 256 takes 0.22 to 0.3 per step, bound by L2, and 4
+//          (2048x2048x2048: 9.8 against Big's 18; 4096x4096x4096: 42)
+// Splitting the contraction costs a launch, 3, and the traffic of its partial
+// sums at 4 TB/s: it pays for long contractions with few outputs
+// (128x1024x8192 in 4 pieces 12.4 against 18.4), seldom else (512x4096x4096
+// in 2 pieces 18.6 against 12.8).
 Plan make_plan(const LinGeom& g, LinOp op) {
-  Plan pl{};
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
   const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
   const int64_t used = g.m < g.ew ? g.m : g.ew;
-  auto count = [&](int tile) {
+  // steps of a tile: with experts, wgrad contracts one's share of the tokens
+  const int64_t all_steps = contract / kPad;
+  const double steps = op == LIN_WGRAD ? static_cast<double>(all_steps) / g.ew : static_cast<double>(all_steps);
+  Plan best{};
+  double best_time = 0.0;
+  auto consider = [&](bool big, int64_t pieces) {
+    Plan pl{};
+    const int tm = big ? Big::TM : Small::TM, tn = big ? Big::TN : Small::TN;
+    // every expert with tokens may leave a part of a tile more
     const int64_t extra = op != LIN_WGRAD && g.e > 0 ? used : 0;
-    pl.tile = tile;
-    pl.tiles_i = (rows + tile - 1) / tile + extra;
-    pl.tiles_j = (cols + tile - 1) / tile;
+    pl.big = big;
+    pl.tiles_i = (rows + tm - 1) / tm + extra;
+    pl.tiles_j = (cols + tn - 1) / tn;
     pl.units = pl.tiles_i * pl.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
-  };
-  count(256);
-  if (pl.units < 256) count(128);
-  pl.splits = 1;
-  pl.split_steps = static_cast<int>(contract / kPad);
-  if (g.e == 0 && pl.units > 0 && pl.units <= 128) {
-    // enough pieces to give every CU a workgroup, of 4 steps at least
-    const int64_t steps = contract / kPad;
-    int64_t s = 256 / pl.units;
-    if (s > steps / 4) s = steps / 4;
-    if (s > 1) {
-      pl.split_steps = static_cast<int>((steps + s - 1) / s);
-      pl.splits = static_cast<int>((steps + pl.split_steps - 1) / pl.split_steps);
+    pl.split_steps = static_cast<int>((all_steps + pieces - 1) / pieces);
+    pl.splits = pieces > 1 ? static_cast<int>((all_steps + pl.split_steps - 1) / pl.split_steps) : 1;
+    const int64_t likely = pl.units - extra * pl.tiles_j / 2;
+    const double rounds = static_cast<double>((likely * pl.splits + 255) / 256);
+    double time = rounds * (big ? 0.8 * steps / pl.splits + 9.0 : (rounds > 1 ? 0.3 : 0.22) * steps / pl.splits + 4.0);
+    if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
+    if (best.units == 0 || time < best_time) {
+      best = pl;
+      best_time = time;
     }
-  }
-  return pl;
+  };
+  consider(false, 1);
+  consider(true, 1);
+  if (g.e == 0)
+    for (int64_t s = 2; s <= 16 && 4 * s <= all_steps; s *= 2) consider(false, s);
+  return best;
 }
 
 }  // namespace
@@ -494,9 +519,9 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   const unsigned grid = static_cast<unsigned>((pl.units * pl.splits + 7) / 8 * 8);
   auto multiply = [&](auto t) {
     using T = decltype(t);
-    auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(grid), dim3(256), 0, s, p); };
-    if (op == LIN_WGRAD) pl.tile == 256 ? launch(k_lin_product<T, 256, true>) : launch(k_lin_product<T, 128, true>);
-    else pl.tile == 256 ? launch(k_lin_product<T, 256, false>) : launch(k_lin_product<T, 128, false>);
+    auto launch = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), 0, s, p); };
+    if (op == LIN_WGRAD) pl.big ? launch(k_lin_product<T, Big, true>, Big::kThreads) : launch(k_lin_product<T, Small, true>, Small::kThreads);
+    else pl.big ? launch(k_lin_product<T, Big, false>, Big::kThreads) : launch(k_lin_product<T, Small, false>, Small::kThreads);
   };
   auto reduce = [&](auto t) {
     using T = decltype(t);

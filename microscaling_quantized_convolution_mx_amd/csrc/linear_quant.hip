@@ -6,8 +6,8 @@
 // The multiplication by a power of two is exact, so the only rounding is the
 // one onto the E2M1 grid.
 //
-// One workgroup takes 128 rows x 128 columns: wave w rows 32w .. 32w+31, in
-// two tiles of 64 columns.  Lane l holds row l%32 and 32 consecutive columns
+// One workgroup takes 128 rows x 128 columns, a wave one tile of 32 x 64:
+// wave w rows 32 (w%4) on, columns 64 (w/4) on.  Lane l holds row l%32 and 32 consecutive columns
 // (l/32): a 1x32 block is one lane's, so its maximum needs no exchange, its
 // 32 codes are one 16-byte store, and the wave's 64 stores are the 1 KiB tile
 // in order.  A 32x32 block is half a wave's: five exchanges.  The column form
@@ -41,15 +41,15 @@ struct QuantParams {
   uint64_t seed;
 };
 
-constexpr int kStageRow = kTileC + 1;  // words between rows in LDS: lanes 32 rows apart hit different banks
+constexpr int kStageRow = kTileC + 1;  // elements between rows in LDS: a column's rows lie in different banks
 
 // VEC: rows start at multiples of 16 bytes.
 template <class T, bool SQUARE, bool SR, bool VEC>
-__global__ __launch_bounds__(256) void k_lin_quantize(const QuantParams p) {
-  __shared__ __attribute__((aligned(16))) uint8_t tiles[4][2][kTileBytes];
+__global__ __launch_bounds__(512) void k_lin_quantize(const QuantParams p) {
+  __shared__ __attribute__((aligned(16))) uint8_t tiles[SQUARE ? 8 : 1][kTileBytes];
   __shared__ __attribute__((aligned(16))) uint8_t rsc[2][kScaleBytes], csc[2][kScaleBytes];
-  __shared__ float stage[VEC ? 1 : 4][VEC ? 1 : 32 * kStageRow];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ T stage[VEC ? 1 : 8][VEC ? 1 : 32 * kStageRow];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3, t = threadIdx.x >> 8;
   // the workgroup's 128 rows: source row and count, padded row, and the
   // matrix' base in the column form
   int64_t row0, prow, crow0 = 0, pr0 = 0;  // pr0: padded row inside the column form's matrix
@@ -79,66 +79,63 @@ __global__ __launch_bounds__(256) void k_lin_quantize(const QuantParams p) {
   const T* src = static_cast<const T*>(p.src) + (row0 + 32 * wave) * p.ld;
   const int nr = static_cast<int>(min<int64_t>(left - 32 * wave, 32));  // rows of the wave, if any
   const int64_t ct0 = static_cast<int64_t>(bx) * 2;  // first column tile
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int64_t c = (ct0 + t) * kTileC + 32 * half;
-    float x[32];
-    if constexpr (VEC) {
-      if (r < nr && c < p.cols) {
-        load32(src + r * p.ld, c, p.cols, true, x);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0.0f;
-      }
+  const int64_t c = (ct0 + t) * kTileC + 32 * half;
+  float x[32];
+  if constexpr (VEC) {
+    if (r < nr && c < p.cols) {
+      load32(src + r * p.ld, c, p.cols, true, x);
     } else {
-      // a lane of its own for each column, so that a load takes one piece of a
-      // row; through LDS to the lane that encodes it
-      float* ls = stage[wave];
-      const int64_t lc = (ct0 + t) * kTileC + lane;
-      const bool in = lc < p.cols && nr > 0;
-      const T* col = src + (in ? lc : 0);
-      T v[32];
-      if (nr > 0) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = col[min(i, nr - 1) * p.ld];
-      }
+      for (int i = 0; i < 32; ++i) x[i] = 0.0f;
+    }
+  } else {
+    // a lane of its own for each column, so that a load takes one piece of a
+    // row; through LDS to the lane that encodes it
+    T* ls = stage[4 * t + wave];
+    const int64_t lc = (ct0 + t) * kTileC + lane;
+    const bool in = lc < p.cols && nr > 0;
+    const T* col = src + (in ? lc : 0);
+    T e[32]{};
+    if (nr > 0) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) ls[i * kStageRow + lane] = in && i < nr ? to_f32(v[i]) : 0.0f;
+      for (int i = 0; i < 32; ++i) e[i] = col[min(i, nr - 1) * p.ld];
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) ls[i * kStageRow + lane] = in && i < nr ? e[i] : T{};
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = to_f32(ls[r * kStageRow + 32 * half + i]);
+    __builtin_amdgcn_wave_barrier();
+  }
+  uint32_t m = amax32(x);
+  if constexpr (SQUARE) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
+  }
+  const uint32_t code = block_code(m);
+  const uint4 w = encode32<SR>(x, code, p.seed, static_cast<uint64_t>(row) * static_cast<uint64_t>(p.cols) + c);
+  if (p.rcodes) {
+    reinterpret_cast<uint4*>(p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes)[lane] = w;
+    rsc[t][lane * 4 + wave] = static_cast<uint8_t>(code);
+  }
+  if constexpr (SQUARE) {
+    if (p.ccodes) {
+      // rows of the tile's two 32x32 blocks in LDS, columns out of it:
+      // each transposing read takes 16 rows for 16 lanes' columns
+      uint8_t* lt = tiles[4 * t + wave];
+      reinterpret_cast<uint4*>(lt)[lane] = w;
       __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = ls[r * kStageRow + 32 * half + i];
-      __builtin_amdgcn_wave_barrier();
-    }
-    uint32_t m = amax32(x);
-    if constexpr (SQUARE) {
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d)));
-    }
-    const uint32_t code = block_code(m);
-    const uint4 w = encode32<SR>(x, code, p.seed, static_cast<uint64_t>(row) * static_cast<uint64_t>(p.cols) + c);
-    if (p.rcodes) {
-      reinterpret_cast<uint4*>(p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes)[lane] = w;
-      rsc[t][lane * 4 + wave] = static_cast<uint8_t>(code);
-    }
-    if constexpr (SQUARE) {
-      if (p.ccodes) {
-        // rows of the tile's two 32x32 blocks in LDS, columns out of it:
-        // each transposing read takes 16 rows for 16 lanes' columns
-        uint8_t* lt = tiles[wave][t];
-        reinterpret_cast<uint4*>(lt)[lane] = w;
-        __builtin_amdgcn_wave_barrier();
-        const uint8_t* b = lt + half * 512 + (lane & 15) * 16 + ((lane >> 4) & 1) * 8;
-        const i32x2v q0 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2v*)(b));
-        const i32x2v q1 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2v*)(b + 256));
-        // column tile of the column form: stripe = 32 source columns, its
-        // columns = the padded rows
-        const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
-        const int64_t pr = pr0 + 32 * wave;
-        uint8_t* dst = p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16;
-        *reinterpret_cast<int4*>(dst) = make_int4(q0.x, q0.y, q1.x, q1.y);
-        // its scale: row r of stripe 2t + half, column half wave%2 of tile wave/2
-        csc[wave >> 1][((wave & 1) * 32 + r) * 4 + 2 * t + half] = static_cast<uint8_t>(code);
-      }
+      const uint8_t* b = lt + half * 512 + (lane & 15) * 16 + ((lane >> 4) & 1) * 8;
+      const i32x2v q0 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2v*)(b));
+      const i32x2v q1 = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2v*)(b + 256));
+      // column tile of the column form: stripe = 32 source columns, its
+      // columns = the padded rows
+      const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
+      const int64_t pr = pr0 + 32 * wave;
+      uint8_t* dst = p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16;
+      *reinterpret_cast<int4*>(dst) = make_int4(q0.x, q0.y, q1.x, q1.y);
+      // its scale: row r of stripe 2t + half, column half wave%2 of tile wave/2
+      csc[wave >> 1][((wave & 1) * 32 + r) * 4 + 2 * t + half] = static_cast<uint8_t>(code);
     }
   }
   __syncthreads();
@@ -148,7 +145,7 @@ __global__ __launch_bounds__(256) void k_lin_quantize(const QuantParams p) {
       uint8_t* d = p.rscales + ((prow / kPad) * p.rkt + ct0) * kScaleBytes;
       reinterpret_cast<uint32_t*>(d)[q] = reinterpret_cast<const uint32_t*>(rsc)[q];
     }
-  } else if (SQUARE && p.ccodes) {
+  } else if (SQUARE && p.ccodes && q < 256) {
     const int i = q - 128;
     uint8_t* d = p.cscales + (((crow0 + ct0 * kTileC) / kPad) * p.ckt + pr0 / kTileC) * kScaleBytes;
     reinterpret_cast<uint32_t*>(d)[i] = reinterpret_cast<const uint32_t*>(csc)[i];
@@ -163,9 +160,9 @@ __device__ __forceinline__ float scale_value(uint32_t code) {
 // Workgroups as in the quantizer.  COLS: from the column form, where a lane's
 // 16 bytes are a column of the matrix.
 template <class T, bool COLS, bool VEC>
-__global__ __launch_bounds__(256) void k_lin_dequantize(const QuantParams p, T* __restrict__ dst) {
+__global__ __launch_bounds__(512) void k_lin_dequantize(const QuantParams p, T* __restrict__ dst) {
   using F = Fmt<FMT_E2M1>;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6 & 3, t = threadIdx.x >> 8;
   int64_t row0, prow, crow0 = 0, pr0;
   int64_t left;
   const uint32_t by = blockIdx.x / p.ncb, bx = blockIdx.x - by * p.ncb;
@@ -189,51 +186,48 @@ __global__ __launch_bounds__(256) void k_lin_dequantize(const QuantParams p, T* 
     const float v = code_value<F>(c & 7u) * scale;
     return from_f32<T>((c & 8u) ? -v : v);
   };
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    if constexpr (!COLS) {
-      // N elements, 16 bytes where rows allow, per lane and pass, so that a
-      // store takes whole pieces of rows
-      constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
-      constexpr int P = kTileC / N;
-      const uint8_t* tile = p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes;
-      const uint8_t* sc = p.rscales + ((prow / kPad) * p.rkt + ct0 + t) * kScaleBytes + wave;
+  if constexpr (!COLS) {
+    // N elements, 16 bytes where rows allow, per lane and pass, so that a
+    // store takes whole pieces of rows
+    constexpr int N = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
+    constexpr int P = kTileC / N;
+    const uint8_t* tile = p.rcodes + ((prow / kTileR + wave) * p.rkt + ct0 + t) * kTileBytes;
+    const uint8_t* sc = p.rscales + ((prow / kPad) * p.rkt + ct0 + t) * kScaleBytes + wave;
 #pragma unroll 8
-      for (int s = 0; s < kTileR * P / 64; ++s) {
-        const int r = (s * 64 + lane) / P, j = (s * 64 + lane) % P * N, half = j >> 5;
-        const uint8_t* at = tile + half * 512 + r * 16 + (j & 31) / 2;
-        uint32_t w;
-        if constexpr (N == 8) w = *reinterpret_cast<const uint32_t*>(at);
-        else if constexpr (N == 4) w = *reinterpret_cast<const uint16_t*>(at);
-        else w = *at >> (4 * (j & 1));
-        const float scale = scale_value(sc[(half * 32 + r) * 4]);
-        struct alignas(N * sizeof(T)) { T e[N]; } y;
+    for (int s = 0; s < kTileR * P / 64; ++s) {
+      const int r = (s * 64 + lane) / P, j = (s * 64 + lane) % P * N, half = j >> 5;
+      const uint8_t* at = tile + half * 512 + r * 16 + (j & 31) / 2;
+      uint32_t w;
+      if constexpr (N == 8) w = *reinterpret_cast<const uint32_t*>(at);
+      else if constexpr (N == 4) w = *reinterpret_cast<const uint16_t*>(at);
+      else w = *at >> (4 * (j & 1));
+      const float scale = scale_value(sc[(half * 32 + r) * 4]);
+      struct alignas(N * sizeof(T)) { T e[N]; } y;
 #pragma unroll
-        for (int i = 0; i < N; ++i) y.e[i] = value(w >> (4 * i), scale);
-        const int64_t c = (ct0 + t) * kTileC + j;
-        if (32 * wave + r >= left) continue;
-        T* d = dst + (row0 + 32 * wave + r) * p.ld + c;
-        if (c + N <= p.cols) {
-          *reinterpret_cast<decltype(y)*>(d) = y;
-        } else {
+      for (int i = 0; i < N; ++i) y.e[i] = value(w >> (4 * i), scale);
+      const int64_t c = (ct0 + t) * kTileC + j;
+      if (32 * wave + r >= left) continue;
+      T* d = dst + (row0 + 32 * wave + r) * p.ld + c;
+      if (c + N <= p.cols) {
+        *reinterpret_cast<decltype(y)*>(d) = y;
+      } else {
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (c + i < p.cols) d[i] = y.e[i];
-        }
+        for (int i = 0; i < N; ++i)
+          if (c + i < p.cols) d[i] = y.e[i];
       }
-    } else {
-      const int r = lane & 31, half = lane >> 5;
-      const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
-      const int64_t pr = pr0 + 32 * wave;
-      const uint4 w = *reinterpret_cast<const uint4*>(p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16);
-      const float scale = scale_value(p.cscales[((stripe / 4) * p.ckt + pr / kTileC) * kScaleBytes + (((pr / 32) & 1) * 32 + r) * 4 + (stripe & 3)]);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      const int64_t c = (ct0 + t) * kTileC + 32 * half + r;
-      if (c >= p.cols) continue;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (32 * wave + i < left) dst[(row0 + 32 * wave + i) * p.ld + c] = value(ww[i >> 3] >> (4 * (i & 7)), scale);
     }
+  } else {
+    const int r = lane & 31, half = lane >> 5;
+    const int64_t stripe = (crow0 + (ct0 + t) * kTileC) / kTileR + half;
+    const int64_t pr = pr0 + 32 * wave;
+    const uint4 w = *reinterpret_cast<const uint4*>(p.ccodes + (stripe * p.ckt + pr / kTileC) * kTileBytes + ((pr / 32) & 1) * 512 + r * 16);
+    const float scale = scale_value(p.cscales[((stripe / 4) * p.ckt + pr / kTileC) * kScaleBytes + (((pr / 32) & 1) * 32 + r) * 4 + (stripe & 3)]);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const int64_t c = (ct0 + t) * kTileC + 32 * half + r;
+    if (c >= p.cols) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (32 * wave + i < left) dst[(row0 + 32 * wave + i) * p.ld + c] = value(ww[i >> 3] >> (4 * (i & 7)), scale);
   }
 }
 
@@ -274,7 +268,7 @@ template <class T> bool vec_rows(const void* p, int64_t ld) {
 template <class T>
 void quantize_as(const QuantParams& p, dim3 grid, int block, bool sr, hipStream_t s) {
   const bool vec = vec_rows<T>(p.src, p.ld);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, p); };
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(512), 0, s, p); };
   if (block == 32) {
     if (sr) vec ? go(k_lin_quantize<T, true, true, true>) : go(k_lin_quantize<T, true, true, false>);
     else vec ? go(k_lin_quantize<T, true, false, true>) : go(k_lin_quantize<T, true, false, false>);
@@ -287,7 +281,7 @@ void quantize_as(const QuantParams& p, dim3 grid, int block, bool sr, hipStream_
 template <class T>
 void dequantize_as(const QuantParams& p, dim3 grid, mx_form form, void* dst, hipStream_t s) {
   const bool vec = vec_rows<T>(dst, p.ld);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, p, static_cast<T*>(dst)); };
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(512), 0, s, p, static_cast<T*>(dst)); };
   if (form == MX_FORM_COLS) go(k_lin_dequantize<T, true, false>);
   else vec ? go(k_lin_dequantize<T, false, true>) : go(k_lin_dequantize<T, false, false>);
 }
