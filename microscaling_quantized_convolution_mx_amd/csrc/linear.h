@@ -126,6 +126,17 @@ __device__ __forceinline__ bool find_segment(const int32_t* __restrict__ off, in
   return false;
 }
 
+// 16 bytes at an address of any alignment: the GPU takes 16-byte accesses that
+// are not aligned, so rows need not start at multiples of 16 bytes.
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(1)));
+__device__ __forceinline__ i32x4 load16(const void* p) { return *static_cast<const i32x4_any*>(p); }
+__device__ __forceinline__ void store16(void* p, i32x4 v) { *static_cast<i32x4_any*>(p) = v; }
+// ... past the caches.  Results that no kernel reads soon are written so: a
+// 16384x8192 dequantization takes 51 us instead of 117, one of 1024x4096 4.6
+// instead of 6.1.
+__device__ __forceinline__ void stream16(void* p, i32x4 v) { __builtin_nontemporal_store(v, static_cast<i32x4_any*>(p)); }
+
 // An element of a matrix of type T as fp32, and back (round to nearest even).
 struct bf16_t { uint16_t v; };
 struct f16_t { _Float16 v; };

@@ -21,7 +21,6 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxWaves = 8;
 constexpr size_t kTokenLds = size_t{48} << 10;  // for a pass' codes and scales, so that three workgroups share a CU
@@ -37,7 +36,6 @@ struct FewParams {
   void* y;
   int64_t ldy;
   int y_dtype;
-  int vec;                 // x's rows start at multiples of 16 bytes
   int tokens, n, k;
   const int32_t* offsets;
   int experts;
@@ -126,9 +124,9 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
         const int r = b / nb, c = b - r * nb;
         const TX* src = static_cast<const TX*>(p.x) + (row0 + t0 + r) * p.ldx;
         float v[32];
-        load32<TX>(src, static_cast<int64_t>(c) * 32, p.k, p.vec != 0, v);
+        load32<TX>(src, static_cast<int64_t>(c) * 32, p.k, v);
         const uint32_t code = block_code(amax32(v));
-        reinterpret_cast<uint4*>(lds)[c * nt + r] = encode32<false>(v, code, 0, 0);
+        reinterpret_cast<uint4*>(lds)[c * nt + r] = encode32<false>(v, code, 0, 0, false);
         sc[c * nt + r] = static_cast<uint8_t>(code);
       }
       __syncthreads();
@@ -273,8 +271,6 @@ hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const
   FewParams p = make_few(g, false, wq, y, y_dtype, ldy, offsets, sn);
   p.x = x;
   p.ldx = ldx;
-  const int64_t size = x_dtype == MX_F32 ? 4 : 2;
-  p.vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * size % 16 == 0;
   const int waves = waves_of(p.kt), most = tokens_per_pass(p.kt);
   p.per_pass = g.m < most ? static_cast<int>(g.m) : most;
   const size_t lds = fused_lds(p.kt, waves, p.per_pass);

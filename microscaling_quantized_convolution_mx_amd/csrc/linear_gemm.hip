@@ -19,7 +19,6 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 template <int I>
 struct Idx {
@@ -39,7 +38,6 @@ struct ProductParams {
   int64_t rows, cols;      // of out (ROWS: rows = tokens; CONTRACT: of one expert's matrix)
   int64_t ld;
   int64_t split_out;       // elements of out from one piece of a split product to the next
-  int vec;                 // out's rows start at multiples of 16 bytes
   int ktiles;              // ROWS and one layer: column tiles to contract
   int tokens;
   const int32_t* offsets;
@@ -76,9 +74,9 @@ __host__ __device__ constexpr int store_bytes() { return 32 * (RN * 32 * static_
 // instruction would write 32 short pieces.  Through LDS, 32 rows at a time,
 // it writes whole rows, 16 bytes per lane.
 // dst: the tile's first output; rleft, cleft: rows and columns from there on
-// that exist; vec: rows start at multiples of 16 bytes.
+// that exist.
 template <int RM, int RN, class U>
-__device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t* buf, U* dst, int64_t ld, bool vec, int64_t rleft,
+__device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t* buf, U* dst, int64_t ld, int64_t rleft,
                                            int64_t cleft, int lane, int wm, int wn) {
   constexpr int W = RN * 32;                                  // columns of the wave
   constexpr int kRow = W * static_cast<int>(sizeof(U)) + 16;  // bytes between rows in LDS
@@ -102,24 +100,17 @@ __device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t*
     __builtin_amdgcn_wave_barrier();
     U* d = dst + static_cast<int64_t>(32 * i) * ld;
     const int64_t left = rleft - 32 * i;
-    if (vec) {
 #pragma unroll
-      for (int s = 0; s < 32 * P / 64; ++s) {
-        const int r = (s * 64 + lane) / P, c = (s * 64 + lane) % P * N;
-        const i32x4 q = *reinterpret_cast<const i32x4*>(buf + r * kRow + c * sizeof(U));
-        if (r < left) {
-          if (c + N <= cleft) *reinterpret_cast<i32x4*>(d + r * ld + c) = q;
-          else {
-            for (int e = 0; e < N; ++e)
-              if (c + e < cleft) d[r * ld + c + e] = reinterpret_cast<const U*>(buf + r * kRow + c * sizeof(U))[e];
-          }
+    for (int s = 0; s < 32 * P / 64; ++s) {
+      const int r = (s * 64 + lane) / P, c = (s * 64 + lane) % P * N;
+      const i32x4 q = *reinterpret_cast<const i32x4*>(buf + r * kRow + c * sizeof(U));
+      if (r < left) {
+        if (c + N <= cleft) {
+          store16(d + r * ld + c, q);
+        } else {
+          for (int e = 0; e < N; ++e)
+            if (c + e < cleft) d[r * ld + c + e] = reinterpret_cast<const U*>(buf + r * kRow + c * sizeof(U))[e];
         }
-      }
-    } else {
-#pragma unroll 4
-      for (int s = 0; s < 32 * W / 64; ++s) {
-        const int r = (s * 64 + lane) / W, c = (s * 64 + lane) % W;
-        if (r < left && c < cleft) d[r * ld + c] = reinterpret_cast<const U*>(buf + r * kRow)[c];
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -396,7 +387,7 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(cons
     wait_barrier<0>();
   }
 
-  store_wave<RM, RN>(acc, lds + wave * store_bytes<T, RN>(), out + orow * p.ld + static_cast<int64_t>(tj) * TN, p.ld, p.vec != 0, rleft,
+  store_wave<RM, RN>(acc, lds + wave * store_bytes<T, RN>(), out + orow * p.ld + static_cast<int64_t>(tj) * TN, p.ld, rleft,
                      cleft, lane, wm, wn);
 }
 
@@ -507,8 +498,6 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.out = split ? workspace : out;
   p.ld = split ? pcols : ld;
   p.split_out = p.rows * pcols;
-  const int64_t size = split || dtype == MX_F32 ? 4 : 2;
-  p.vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld * size % 16 == 0;
   p.tokens = static_cast<int>(g.m);
   p.offsets = offsets;
   p.experts = g.e;
