@@ -67,22 +67,24 @@ struct Segment {
 };
 
 #ifdef __HIPCC__
-// Inclusive scans over the wave's 64 lanes.
-__device__ __forceinline__ int wave_scan_max(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int t = __shfl_up(v, d);
-    v = lane >= d ? max(v, t) : v;
-  }
+// Inclusive scans over the wave's 64 lanes (of values >= 0 for the maximum):
+// within rows of 16 lanes, then each row's last value into the next row, then
+// the first half's into the second.
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));  // row_shr:1
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));  // row_shr:2
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));  // row_shr:4
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));  // row_shr:8
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));  // row_bcast:15
+  v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));  // row_bcast:31
   return v;
 }
-__device__ __forceinline__ int wave_scan_add(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int t = __shfl_up(v, d);
-    v = lane >= d ? v + t : v;
-  }
-  return v;
+__device__ __forceinline__ int wave_scan_max(int v) {
+  return wave_scan(v, [](int a, int b) { return max(a, b); });
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+  return wave_scan(v, [](int a, int b) { return a + b; });
 }
 
 // Finds the expert that holds unit `target` when expert e's tokens make
@@ -100,27 +102,25 @@ __device__ __forceinline__ bool find_segment(const int32_t* __restrict__ off, in
   for (int base = 0; base < experts; base += 64) {
     const int e = base + lane;
     const int raw = e < experts ? min(max(off[e + 1], 0), m) : 0;
-    const int end = max(wave_scan_max(raw, lane), start);
-    int first = __shfl_up(end, 1);
-    first = lane == 0 ? start : first;
+    const int end = max(wave_scan_max(raw), start);
+    const int first = __builtin_amdgcn_update_dpp(start, end, 0x138, 0xF, 0xF, false);  // wave_shr:1
     const int len = end - first;
     const int u = per > 0 ? (len + per - 1) / per : (e < experts ? 1 : 0);
     const int p = (len + kPad - 1) / kPad;
-    const int us = wave_scan_add(u, lane), ps = wave_scan_add(p, lane);
-    const bool here = target >= units + us - u && target < units + us;
-    const uint64_t hit = __ballot(here);
+    const int us = wave_scan_add(u), ps = wave_scan_add(p);
+    const uint64_t hit = __ballot(target >= units + us - u && target < units + us);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       seg.e = base + l;
-      seg.len = __shfl(len, l);
-      seg.row0 = __shfl(first, l);
-      seg.prow = static_cast<int64_t>(pads + __shfl(ps - p, l)) * kPad;
-      seg.unit = target - (units + __shfl(us - u, l));
+      seg.len = __builtin_amdgcn_readlane(len, l);
+      seg.row0 = __builtin_amdgcn_readlane(first, l);
+      seg.prow = static_cast<int64_t>(pads + __builtin_amdgcn_readlane(ps - p, l)) * kPad;
+      seg.unit = target - (units + __builtin_amdgcn_readlane(us - u, l));
       return true;
     }
-    units += __shfl(us, 63);
-    pads += __shfl(ps, 63);
-    start = __shfl(end, 63);
+    units += __builtin_amdgcn_readlane(us, 63);
+    pads += __builtin_amdgcn_readlane(ps, 63);
+    start = __builtin_amdgcn_readlane(end, 63);
   }
   if (total) *total = units;
   return false;

@@ -8,6 +8,7 @@
 // so one kernel serves all three.  With experts, fwd and dgrad take the rows
 // of `a` in segments with a weight matrix each (ROWS), wgrad the columns in
 // segments with an output matrix each (CONTRACT).
+#include "internal.h"
 #include "linear.h"
 
 #include <type_traits>
@@ -38,6 +39,7 @@ struct ProductParams {
   int64_t rows, cols;      // of out (ROWS: rows = tokens; CONTRACT: of one expert's matrix)
   int64_t ld;
   int64_t split_out;       // elements of out from one piece of a split product to the next
+  int stream;              // out is written past the caches
   int ktiles;              // ROWS and one layer: column tiles to contract
   int tokens;
   const int32_t* offsets;
@@ -75,7 +77,8 @@ __host__ __device__ constexpr int store_bytes() { return 32 * (RN * 32 * static_
 // it writes whole rows, 16 bytes per lane.
 // dst: the tile's first output; rleft, cleft: rows and columns from there on
 // that exist.
-template <int RM, int RN, class U>
+// STREAM: past the caches.
+template <bool STREAM, int RM, int RN, class U>
 __device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t* buf, U* dst, int64_t ld, int64_t rleft,
                                            int64_t cleft, int lane, int wm, int wn) {
   constexpr int W = RN * 32;                                  // columns of the wave
@@ -106,7 +109,8 @@ __device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t*
       const i32x4 q = *reinterpret_cast<const i32x4*>(buf + r * kRow + c * sizeof(U));
       if (r < left) {
         if (c + N <= cleft) {
-          store16(d + r * ld + c, q);
+          if constexpr (STREAM) stream16(d + r * ld + c, q);
+          else store16(d + r * ld + c, q);
         } else {
           for (int e = 0; e < N; ++e)
             if (c + e < cleft) d[r * ld + c + e] = reinterpret_cast<const U*>(buf + r * kRow + c * sizeof(U))[e];
@@ -387,8 +391,10 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(cons
     wait_barrier<0>();
   }
 
-  store_wave<RM, RN>(acc, lds + wave * store_bytes<T, RN>(), out + orow * p.ld + static_cast<int64_t>(tj) * TN, p.ld, rleft,
-                     cleft, lane, wm, wn);
+  T* tile = out + orow * p.ld + static_cast<int64_t>(tj) * TN;
+  uint8_t* buf = lds + wave * store_bytes<T, RN>();
+  if (p.stream) store_wave<true, RM, RN>(acc, buf, tile, p.ld, rleft, cleft, lane, wm, wn);
+  else store_wave<false, RM, RN>(acc, buf, tile, p.ld, rleft, cleft, lane, wm, wn);
 }
 
 // Sums the pieces of a split product in their order, 4 columns per thread.
@@ -498,6 +504,12 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.out = split ? workspace : out;
   p.ld = split ? pcols : ld;
   p.split_out = p.rows * pcols;
+  // outputs that the last-level cache cannot hold (16 experts' 4096x4096 fp32
+  // gradients: 218 us, 259 through the caches); smaller ones stay in it for the
+  // next layer (4096x4096 bf16: 46 us with a quantization of the result, 48 past
+  // the caches)
+  const size_t bytes = static_cast<size_t>(p.rows) * p.cols * (op == LIN_WGRAD ? g.ew : 1) * (dtype == MX_F32 ? 4 : 2);
+  p.stream = !split && bytes >= kStreamOutBytes;
   p.tokens = static_cast<int>(g.m);
   p.offsets = offsets;
   p.experts = g.e;
