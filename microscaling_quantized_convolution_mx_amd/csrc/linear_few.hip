@@ -260,10 +260,10 @@ bool lin_fused(const LinGeom& g) {
   return g.e == 0 ? g.m <= t : lin_few(g);
 }
 
-// Two passes of tokens, or experts with few tokens each.  (64x4096x4096 takes
-// 7.7 us here and 11.6 in 128x128 tiles, 64x1024x1024 6.7 and 6.3; a third
-// pass, 96x4096x4096 10.3 and 11.7, 96x1024x1024 8.9 and 6.3.)
-bool lin_few(const LinGeom& g) { return g.e == 0 ? g.m <= 64 : g.m <= 16 * static_cast<int64_t>(g.e); }
+// One pass of tokens, or experts with few tokens each.  (32x4096x4096 takes 5.1
+// us here and 7.8 in 64x64 tiles, 64x4096x4096 7.7 and 7.9, 64x1024x1024 6.7
+// and 4.5.)
+bool lin_few(const LinGeom& g) { return g.e == 0 ? g.m <= 32 : g.m <= 16 * static_cast<int64_t>(g.e); }
 
 hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
                             void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s) {

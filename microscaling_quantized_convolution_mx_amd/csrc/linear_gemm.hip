@@ -63,8 +63,10 @@ struct Shape {
   static constexpr int TM = M, TN = N, WM = A, WN = B, kStages = S;
   static constexpr int kThreads = 64 * A * B;
 };
+// Big for the MFMA's rate, Tiny for short latency (make_plan).
 using Big = Shape<256, 256, 2, 2, 4>;
 using Small = Shape<128, 128, 2, 2, 4>;
+using Tiny = Shape<64, 64, 2, 2, 4>;
 
 // LDS that a wave's stores go through: 32 rows of its outputs, 16 bytes apart
 // from each other so that neither the writes nor the reads conflict.
@@ -157,8 +159,9 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(cons
   constexpr int RM = TM / WM / 32, RN = TN / WN / 32;  // MFMA rows and columns of a wave
   constexpr int kWaves = WM * WN;
   constexpr int kOpndA = TM / 32 * kStepTiles * kTileBytes, kOpndB = TN / 32 * kStepTiles * kTileBytes;
-  constexpr int kGroupsA = TM / kPad * kStepTiles, kGroups = (TM + TN) / kPad * kStepTiles;  // 256-byte groups of scales
-  constexpr int kScales = kOpndA + kOpndB;                                                  // their place in a stage
+  // 256-byte groups of scales, of 128 rows each (of which a tile of 64 uses half)
+  constexpr int kGroupsA = (TM + kPad - 1) / kPad * kStepTiles, kGroups = kGroupsA + (TN + kPad - 1) / kPad * kStepTiles;
+  constexpr int kScales = kOpndA + kOpndB;  // their place in a stage
   constexpr int kStage = kScales + kGroups * kScaleBytes;
   constexpr int kStoreBytes = kWaves * store_bytes<T, RN>();
   __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage > kStoreBytes ? kStages * kStage : kStoreBytes];
@@ -313,14 +316,16 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(cons
     const uint8_t* at = s + ((stripe >> 2) * kStepTiles + j) * kScaleBytes + 4 * lane + (stripe & 3);
     return n == 4 ? *reinterpret_cast<const int*>(at) : n == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
   };
+  // (the tile's first stripe among its 128 rows' four)
+  const int sa0 = TM < kPad ? static_cast<int>(arow / kTileR & 3) : 0, sb0 = TN < kPad ? static_cast<int>(brow / kTileR & 3) : 0;
   // read r of slice j: the scales, then the tiles in the order of their use
   constexpr int kReads = RM + RN + 2;
   auto read = [&](const uint8_t* st, int j, Frags& f, auto r) {
     constexpr int R = decltype(r)::value;
     if constexpr (R == 0) {
-      f.sa = read_scales(st + kScales, wm * RM, RM, j);
+      f.sa = read_scales(st + kScales, sa0 + wm * RM, RM, j);
     } else if constexpr (R == 1) {
-      f.sb = read_scales(st + kScales + kGroupsA * kScaleBytes, wn * RN, RN, j);
+      f.sb = read_scales(st + kScales + kGroupsA * kScaleBytes, sb0 + wn * RN, RN, j);
     } else if constexpr (R == 2 || R >= RN + 3) {
       constexpr int I = R == 2 ? 0 : R - RN - 2;
       f.a[I] = operand(reinterpret_cast<const i32x4*>(st + ((wm * RM + I) * kStepTiles + j) * kTileBytes)[lane]);
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin_product(cons
       const uint32_t next = cur == (kStages - 1) * kStage ? 0 : cur + kStage;
       static_for<kSlots>([&](auto n) {
         mfma(fA, n);
-        deal(n, Idx<0>{}, Idx<kReads>{}, Idx<kSlots * 3 / 4>{}, [&](auto r) { read(lds + cur, 1, fB, r); });
+        deal(n, Idx<0>{}, Idx<kReads>{}, Idx<(kSlots * 3 + 3) / 4>{}, [&](auto r) { read(lds + cur, 1, fB, r); });
         deal(n, Idx<kHalf>{}, Idx<kCopies - kHalf>{}, Idx<kSlots>{}, [&](auto l) { copy(last, l); });
         __builtin_amdgcn_sched_barrier(0);
       });
@@ -413,22 +418,24 @@ __global__ __launch_bounds__(256) void k_lin_reduce(const float* __restrict__ pa
 }
 
 struct Plan {
-  bool big;     // Big or Small tiles
+  int shape;    // 0: Tiny, 1: Small, 2: Big
   int64_t tiles_i, tiles_j;
   int splits, split_steps;
   int64_t units;  // workgroups, at most
 };
 
 // Tiles and split by estimated time, in us, fitted to measured products (bf16
-// outputs, 2048^3 to 8192^3 and 128..2048 rows of 1024..8192 columns):
-//   Big    a round of 256 workgroups takes 0.8 per step and 9 for its first
-//          loads and its stores (4096x4096x4096: 39)
-//   Small  a round of 256 takes 0.22 to 0.3 per step, bound by L2, and 4
-//          (2048x2048x2048: 9.8 against Big's 18; 4096x4096x4096: 42)
+// outputs, 64 to 8192 rows and 512 to 8192 columns).  A round is 256
+// workgroups, one per CU:
+//   Big    9 for the first loads and the stores, 0.8 per step and round, bound
+//          by the MFMA (4096x4096x4096 39, Small 42)
+//   Small  5, and 0.28 per step and round, bound by L2 (2048^3 9.7, Tiny 11.8,
+//          Big 18)
+//   Tiny   3.6, and 0.13 per step and round, bound by the latency of a step
+//          (777x1000x520 4.6, Small 7.4; 301x2500x1999 6.3, Small 9.3)
 // Splitting the contraction costs a launch, 3, and the traffic of its partial
-// sums at 4 TB/s: it pays for long contractions with few outputs
-// (128x1024x8192 in 4 pieces 12.4 against 18.4), seldom else (512x4096x4096
-// in 2 pieces 18.6 against 12.8).
+// sums at 4 TB/s: it pays for long contractions with few outputs, seldom else
+// (512x4096x4096 by Small 12.7, in 2 pieces 18.3).
 Plan make_plan(const LinGeom& g, LinOp op) {
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
   const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
@@ -438,30 +445,29 @@ Plan make_plan(const LinGeom& g, LinOp op) {
   const double steps = op == LIN_WGRAD ? static_cast<double>(all_steps) / g.ew : static_cast<double>(all_steps);
   Plan best{};
   double best_time = 0.0;
-  auto consider = [&](bool big, int64_t pieces) {
+  auto consider = [&](int shape, int64_t pieces) {
     Plan pl{};
-    const int tm = big ? Big::TM : Small::TM, tn = big ? Big::TN : Small::TN;
+    const int tm = shape == 2 ? Big::TM : shape == 1 ? Small::TM : Tiny::TM, tn = shape == 2 ? Big::TN : shape == 1 ? Small::TN : Tiny::TN;
     // every expert with tokens may leave a part of a tile more
     const int64_t extra = op != LIN_WGRAD && g.e > 0 ? used : 0;
-    pl.big = big;
+    pl.shape = shape;
     pl.tiles_i = (rows + tm - 1) / tm + extra;
     pl.tiles_j = (cols + tn - 1) / tn;
     pl.units = pl.tiles_i * pl.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
     pl.split_steps = static_cast<int>((all_steps + pieces - 1) / pieces);
     pl.splits = pieces > 1 ? static_cast<int>((all_steps + pl.split_steps - 1) / pl.split_steps) : 1;
     const int64_t likely = pl.units - extra * pl.tiles_j / 2;
-    const double rounds = static_cast<double>((likely * pl.splits + 255) / 256);
-    double time = rounds * (big ? 0.8 * steps / pl.splits + 9.0 : (rounds > 1 ? 0.3 : 0.22) * steps / pl.splits + 4.0);
+    const double rounds = static_cast<double>((likely * pl.splits + 255) / 256), each = steps / pl.splits;
+    double time = shape == 2 ? rounds * (9.0 + 0.8 * each) : shape == 1 ? 5.0 + rounds * 0.28 * each : 3.6 + rounds * 0.13 * each;
     if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
     if (best.units == 0 || time < best_time) {
       best = pl;
       best_time = time;
     }
   };
-  consider(false, 1);
-  consider(true, 1);
+  for (int shape : {0, 1, 2}) consider(shape, 1);
   if (g.e == 0)
-    for (int64_t s = 2; s <= 16 && 4 * s <= all_steps; s *= 2) consider(false, s);
+    for (int64_t s = 2; s <= 16 && 4 * s <= all_steps; s *= 2) consider(0, s);
   return best;
 }
 
@@ -521,8 +527,12 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   auto multiply = [&](auto t) {
     using T = decltype(t);
     auto launch = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), 0, s, p); };
-    if (op == LIN_WGRAD) pl.big ? launch(k_lin_product<T, Big, true>, Big::kThreads) : launch(k_lin_product<T, Small, true>, Small::kThreads);
-    else pl.big ? launch(k_lin_product<T, Big, false>, Big::kThreads) : launch(k_lin_product<T, Small, false>, Small::kThreads);
+    auto with = [&](auto contract) {
+      constexpr bool C = decltype(contract)::value;
+      pl.shape == 2 ? launch(k_lin_product<T, Big, C>, Big::kThreads)
+                    : pl.shape == 1 ? launch(k_lin_product<T, Small, C>, Small::kThreads) : launch(k_lin_product<T, Tiny, C>, Tiny::kThreads);
+    };
+    op == LIN_WGRAD ? with(std::true_type{}) : with(std::false_type{});
   };
   auto reduce = [&](auto t) {
     using T = decltype(t);
