@@ -55,14 +55,16 @@ class mx_grad_list(ctypes.Structure):
 
 
 _lib = None
+_torch = None
 _dtypes = None
 
 
 def _load():
     """The library with the argument types of these entry points."""
-    global _lib, _dtypes
+    global _lib, _torch, _dtypes
     if _lib is None:
         import torch
+        _torch = torch
         _dtypes = {torch.float32: MX_F32, torch.bfloat16: MX_BF16, torch.float16: MX_F16}
         L = _mx.lib()
         D, Q, P = ctypes.POINTER(mx_linear_desc), ctypes.POINTER(mx_linear_qtensor), ctypes.c_void_p
@@ -100,10 +102,9 @@ def _matrix(t, shape, what: str):
     """(address, mx_dtype, row stride) of a tensor after checking it: nothing
     that the kernels could not read reaches them.  None passes through as a
     NULL float32 matrix (the library reports MX_ERR_NULL)."""
-    import torch
     if t is None:
         return None, MX_F32, shape[-1]
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     dt = _dtypes.get(t.dtype)
     if dt is None:
@@ -112,28 +113,26 @@ def _matrix(t, shape, what: str):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what}: must be in device memory, got a {t.device.type} tensor")
+    if t.is_contiguous():
+        return t.data_ptr() or None, dt, shape[-1]
     st = t.stride()
-    rows = shape[-2]
-    ld = st[-2] if rows > 1 or (len(shape) == 3 and shape[0] > 1) else shape[-1]
-    if t.numel():
-        if st[-1] != 1 and shape[-1] > 1:
-            raise ValueError(f"{what}: the last dimension must have stride 1, got {st[-1]}")
-        if len(shape) == 3 and shape[0] > 1:
-            ld = st[1] if rows > 1 else st[0]
-            if st[0] != rows * ld:
-                raise ValueError(f"{what}: experts must follow each other without a gap")
-        if ld < shape[-1]:
-            raise ValueError(f"{what}: rows overlap (row stride {ld}, {shape[-1]} columns)")
-    else:
-        ld = shape[-1]
+    rows, cols = shape[-2], shape[-1]
+    if st[-1] != 1 and cols > 1:
+        raise ValueError(f"{what}: the last dimension must have stride 1, got {st[-1]}")
+    ld = st[-2] if rows > 1 else cols
+    if len(shape) == 3 and shape[0] > 1:
+        ld = st[1] if rows > 1 else st[0]
+        if st[0] != rows * ld:
+            raise ValueError(f"{what}: experts must follow each other without a gap")
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap (row stride {ld}, {cols} columns)")
     return t.data_ptr() or None, dt, ld
 
 
 def _offsets(d: mx_linear_desc, t):
     if d.experts <= 0 or t is None:
         return None
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+    if not isinstance(t, _torch.Tensor) or t.dtype != _torch.int32 or not t.is_contiguous():
         raise ValueError("offsets: must be a contiguous int32 tensor")
     if t.numel() != d.experts + 1:
         raise ValueError(f"offsets: {t.numel()} values, the call needs {d.experts + 1}")
@@ -171,7 +170,7 @@ class LinearQTensor:
     def __init__(self, d: mx_linear_desc, role: int, device="cuda", rows: bool = True, cols: bool | None = None):
         """cols: by default where the descriptor has that form (block 32)."""
         import torch
-        self.role = role
+        self.role, self.desc = role, bytes(d)
         cols = d.block == 32 if cols is None else cols
         self.bytes, self.buffers = {}, {}
         for form, wanted in ((MX_FORM_ROWS, rows), (MX_FORM_COLS, cols)):
@@ -193,12 +192,13 @@ def _q(q, d: mx_linear_desc, role: int, forms, what: str):
         return q
     if not isinstance(q, LinearQTensor):
         raise TypeError(f"{what}: expected a LinearQTensor or an mx_linear_qtensor, got {type(q).__name__}")
+    same = q.role == role and q.desc == bytes(d)  # sized for this very call
     L = _lib
     for form in forms:
         have = q.bytes.get(form)
         if have is None:
             raise ValueError(f"{what}: has no {'column' if form else 'row'} form")
-        if have[0] < L.mx_linear_code_bytes(d, role, form) or have[1] < L.mx_linear_scale_bytes(d, role, form):
+        if not same and (have[0] < L.mx_linear_code_bytes(d, role, form) or have[1] < L.mx_linear_scale_bytes(d, role, form)):
             raise ValueError(f"{what}: {have[0]} bytes of codes, the call needs {L.mx_linear_code_bytes(d, role, form)}")
     if not q.is_cuda:
         raise ValueError(f"{what}: must be in device memory")
