@@ -10,8 +10,9 @@
 // any finite fp32 fit, and the adds are far below the vector units' rate.
 //
 // The tensors' addresses and sizes travel in the kernel's arguments, so no
-// table has to be copied to the device.  Work is dealt in chunks of kChunk
-// elements over all tensors; a workgroup takes every gridDim.x-th chunk.
+// table has to be copied to the device.  Work is dealt in chunks over all
+// tensors; a workgroup takes every gridDim.x-th chunk.  Chunks are of 8192
+// elements, or of 2048 where that leaves CUs idle.
 #include "internal.h"
 #include "linear.h"
 
@@ -20,7 +21,7 @@ namespace {
 
 constexpr int kTensors = 96;       // per launch: the arguments stay below 4 KiB
 constexpr int kThreads = 256;
-constexpr int kChunk = 8192;       // elements
+constexpr int kChunk = 8192, kSmallChunk = 2048;  // elements
 constexpr int kMaxGroups = 1024;   // workgroups, and partials, per launch
 
 struct Batch {
@@ -30,6 +31,7 @@ struct Batch {
   int32_t first[kTensors + 1];  // first chunk of each tensor
   uint8_t dtype[kTensors];
   int32_t count;
+  int32_t chunk;   // elements of a chunk
   int32_t stream;  // whether the outputs pass the last-level cache
 };
 
@@ -42,15 +44,14 @@ __device__ __forceinline__ void unpack(uint4 v, float* x) {
   for (int i = 0; i < Pack<T>::N; ++i) x[i] = to_f32(e[i]);
 }
 
-// the tensor of chunk c
+// the tensor of chunk c: the last one that starts at it or before.  Every lane
+// compares two of them.
 __device__ __forceinline__ int tensor_of(const Batch& b, int c) {
-  int lo = 0, hi = b.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (b.first[mid] <= c) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  static_assert(kTensors <= 128);
+  const int lane = threadIdx.x & 63;
+  const uint64_t lo = __ballot(lane < b.count && b.first[min(lane, kTensors)] <= c);
+  const uint64_t hi = __ballot(lane + 64 < b.count && b.first[min(lane + 64, kTensors)] <= c);
+  return __popcll(lo) + __popcll(hi) - 1;
 }
 
 // Elements before the first multiple of 16 bytes (n at most).  Gradients that
@@ -126,8 +127,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_sum(const Batch b, double* __
   double s = 0.0;
   for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
     const int t = tensor_of(b, c);
-    const int64_t at = static_cast<int64_t>(c - b.first[t]) * kChunk;
-    const int64_t n = min(static_cast<int64_t>(kChunk), b.numel[t] - at);
+    const int64_t at = static_cast<int64_t>(c - b.first[t]) * b.chunk;
+    const int64_t n = min(static_cast<int64_t>(b.chunk), b.numel[t] - at);
     if (b.dtype[t] == MX_BF16) s += sum_chunk(static_cast<const bf16_t*>(b.grad[t]) + at, n);
     else if (b.dtype[t] == MX_F16) s += sum_chunk(static_cast<const f16_t*>(b.grad[t]) + at, n);
     else s += sum_chunk(static_cast<const float*>(b.grad[t]) + at, n);
@@ -150,8 +151,8 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(const Batch b, const dou
   for (int c = blockIdx.x; c < b.first[b.count]; c += gridDim.x) {
     const int t = tensor_of(b, c);
     if (f == 1.0f && b.grad[t] == b.out[t]) continue;
-    const int64_t at = static_cast<int64_t>(c - b.first[t]) * kChunk;
-    const int64_t n = min(static_cast<int64_t>(kChunk), b.numel[t] - at);
+    const int64_t at = static_cast<int64_t>(c - b.first[t]) * b.chunk;
+    const int64_t n = min(static_cast<int64_t>(b.chunk), b.numel[t] - at);
     if (b.dtype[t] == MX_BF16) scale_chunk(static_cast<const bf16_t*>(b.grad[t]) + at, static_cast<bf16_t*>(b.out[t]) + at, n, f, b.stream != 0);
     else if (b.dtype[t] == MX_F16) scale_chunk(static_cast<const f16_t*>(b.grad[t]) + at, static_cast<f16_t*>(b.out[t]) + at, n, f, b.stream != 0);
     else scale_chunk(static_cast<const float*>(b.grad[t]) + at, static_cast<float*>(b.out[t]) + at, n, f, b.stream != 0);
@@ -160,13 +161,14 @@ __global__ __launch_bounds__(kThreads) void k_grad_clip(const Batch b, const dou
 
 // The next batch of non-empty tensors from i on.  The caller has checked that
 // all chunks together fit an int32.
-void fill(const mx_grad_list* l, int& i, Batch& b, bool stream = false) {
+void fill(const mx_grad_list* l, int& i, Batch& b, int chunk, bool stream = false) {
+  b.chunk = chunk;
   b.stream = stream ? 1 : 0;
   b.count = 0;
   int64_t chunks = 0;
   for (; i < l->count && b.count < kTensors; ++i) {
     if (l->numel[i] <= 0) continue;
-    const int64_t more = (l->numel[i] + kChunk - 1) / kChunk;
+    const int64_t more = (l->numel[i] + chunk - 1) / chunk;
     b.grad[b.count] = l->grads[i];
     b.out[b.count] = l->out ? l->out[i] : nullptr;
     b.numel[b.count] = l->numel[i];
@@ -192,9 +194,12 @@ hipError_t launch_grad_clip(const mx_grad_list* l, bool clip, float max_norm, fl
   double* partial = static_cast<double*>(workspace);
   int partials = 0;
   static_assert(sizeof(Batch) + 64 <= 4096);
+  int64_t total = 0;
+  for (int i = 0; i < l->count; ++i) total += l->numel[i];
+  const int chunk = total < static_cast<int64_t>(kChunk) * kMaxGroups ? kSmallChunk : kChunk;
   Batch b;
   for (int i = 0; i < l->count;) {
-    fill(l, i, b);
+    fill(l, i, b, chunk);
     if (b.count == 0) break;
     const unsigned wgs = groups(b);
     hipLaunchKernelGGL(k_grad_sum, dim3(wgs), dim3(kThreads), 0, s, b, partial + partials);
@@ -206,7 +211,7 @@ hipError_t launch_grad_clip(const mx_grad_list* l, bool clip, float max_norm, fl
   size_t bytes = 0;
   for (int i = 0; i < l->count; ++i) bytes += static_cast<size_t>(l->numel[i]) * (l->dtypes[i] == MX_F32 ? 4 : 2);
   for (int i = 0; clip && i < l->count;) {
-    fill(l, i, b, bytes > kStreamOutBytes);
+    fill(l, i, b, chunk, bytes > kStreamOutBytes);
     if (b.count == 0) break;
     hipLaunchKernelGGL(k_grad_clip, dim3(groups(b)), dim3(kThreads), 0, s, b, partial, partials, max_norm, norm, first ? 1 : 0);
     first = false;
