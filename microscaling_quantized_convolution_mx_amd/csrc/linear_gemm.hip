@@ -8,6 +8,15 @@
 // so one kernel serves all three.  With experts, fwd and dgrad take the rows
 // of `a` in segments with a weight matrix each (ROWS), wgrad the columns in
 // segments with an output matrix each (CONTRACT).
+//
+// Measured (bf16 outputs, fp32 for wgrad): 8192x8192x8192 234 to 270 us, 4.1 to
+// 4.7 PFLOP/s; 16384x4096x4096 forward 138, weight gradient 118; 4096^3 37.
+// The MFMA is busy 61% of a workgroup's time, at 1.9 GHz of 2.4: the same
+// loop without its copies and reads reaches 5.7 PFLOP/s at 1.7 GHz, and other
+// tilings with other waits (256x256 by 8 waves, 256x128 by two workgroups per
+// CU) come out within 3% of this one, so what bounds a large product is the
+// power that operands and MFMA draw.  A single round (4096^3) also waits 9 us
+// for its first operands and its stores.
 #include "internal.h"
 #include "linear.h"
 

@@ -17,8 +17,11 @@
 // back through the transposing 4-bit LDS read.  Scale bytes are gathered in
 // LDS, since 128 rows share a dword.
 //
-// Bound by memory traffic for RNE; SR adds a 64-bit multiplicative hash per
-// two elements and is bound by those integer operations.
+// Bound by memory traffic for RNE: 16384x8192 bf16 67 us for the row form (5.0
+// TB/s, a large copy's rate), 83 for both.  SR adds a 64-bit multiplicative hash
+// per two elements and is bound by those integer operations, 1.0e12 elements/s:
+// 131 us; neither other ways to encode nor half as many registers change that.
+// Dequantizing to bf16 takes 51 us (6.7 TB/s).
 #include <type_traits>
 
 #include "linear.h"

@@ -134,3 +134,17 @@ def test_results_repeat_bit_for_bit():
     first = clip([t.clone() for t in g], 0.5)
     for _ in range(3):
         assert clip([t.clone() for t in g], 0.5) == first
+
+
+def test_outputs_past_the_cache():
+    """Lists of more than 256 MiB; checked on the device, as their size asks."""
+    g = [torch.randn(50_000_001, device=DEV), torch.randn(30_000_003, device=DEV).bfloat16(), torch.randn(7, device=DEV),
+         torch.randn(15_000_000, device=DEV)]
+    outs = [torch.full_like(t, 5.0) for t in g]
+    got = clip(g, 10.0, outs)
+    want = math.sqrt(sum(float(t.double().square().sum()) for t in g))
+    assert abs(got - want) <= 2.0 ** -23 * want
+    f = min(1.0, 10.0 / (want + 1e-6))
+    for t, o in zip(g, outs):
+        ref = t.double() * f
+        assert bool(((o.double() - ref).abs() <= ref.abs() * (5 * 2.0 ** -24 + UNIT[t.dtype] * 1.01) + 2.0 ** -134).all())

@@ -502,3 +502,105 @@ def test_graph_and_stream():
         torch.cuda.synchronize()
         for a, b in zip(got, out):
             assert torch.equal(a, b) and not bool(torch.isnan(a).any())
+
+
+# ---------------------------------------------------------------- sizes that take the larger tiles
+
+def sampled_case(m, n, k, dt, lens=None, seed=1, rows=96, fwd=True, dgrad=True, wgrad=True):
+    """The products on rows (of y, dx and dw) drawn at random, the first and the last among them."""
+    e = len(lens) if lens is not None else 0
+    off = offsets_of(lens) if e else None
+    segs = R.segments(m, off.tolist() if e else None)
+    d = mx.linear_desc(m, n, k, experts=e)
+    g = np.random.default_rng(seed)
+    x, dy, w = rand(seed, m, k, dt=dt), rand(seed + 1, m, n, dt=dt), rand(seed + 2, max(e, 1), n, k, dt=dt)
+    ws = workspace(d)
+    wq = quantize(d, WEIGHT, (w if e else w[0]).to(DEV))
+    xq = quantize(d, ACT, x.to(DEV), off=off)
+    xv, wv = R.quantize_tokens(f64(x), 32, off.tolist() if e else None), [R.quantize(f64(a), 32)[2] for a in w]
+    pick = np.unique(np.concatenate([g.integers(0, m, rows), [0, m - 1]]))
+
+    def check(got, p, q, c, what):
+        ref, mags = p @ q, np.abs(p) @ np.abs(q)
+        assert np.all(np.abs(got - ref) <= R.bound(c, mags, ref, dt)), what
+
+    def rows_of(t, i):
+        return f64(t[torch.from_numpy(i).to(DEV)])
+    if fwd:
+        y = torch.full((m, n), float("nan"), dtype=TYPES[dt], device=DEV)
+        mx.mx_linear_fwd(d, wq, xq, y, ws, offsets=off)
+        assert not bool(torch.isnan(y).any())
+        for i, (a, b) in enumerate(segs):
+            at = pick[(pick >= a) & (pick < b)]
+            check(rows_of(y, at), xv[at], wv[i].T, k, f"y of {i}")
+        del y
+    if not (dgrad or wgrad):
+        return
+    dyq = quantize(d, GRAD, dy.to(DEV), off=off)
+    dyv = R.quantize_tokens(f64(dy), 32, off.tolist() if e else None)
+    if dgrad:
+        dx = torch.full((m, k), float("nan"), dtype=TYPES[dt], device=DEV)
+        mx.mx_linear_dgrad(d, wq, dyq, dx, ws, offsets=off)
+        assert not bool(torch.isnan(dx).any())
+        for i, (a, b) in enumerate(segs):
+            at = pick[(pick >= a) & (pick < b)]
+            check(rows_of(dx, at), dyv[at], wv[i], n, f"dx of {i}")
+    if wgrad:
+        dw = torch.full((max(e, 1), n, k), float("nan"), dtype=TYPES[dt], device=DEV)
+        mx.mx_linear_wgrad(d, dyq, xq, dw if e else dw[0], ws, offsets=off)
+        assert not bool(torch.isnan(dw).any())
+        at = np.unique(np.concatenate([g.integers(0, n, rows), [0, n - 1]]))
+        for i, (a, b) in enumerate(segs):
+            check(rows_of(dw[i], at), dyv[a:b, at].T, xv[a:b], b - a, f"dw of {i}")
+
+
+@pytest.mark.parametrize("m,n,k,dt", [
+    (1100, 4000, 1000, "bf16"), (1100, 4001, 1000, "f32"),     # 128x128 tiles
+    (4100, 4200, 2100, "bf16"), (4099, 4201, 2051, "f16"),     # 256x256 tiles, ragged at both edges, an odd number of steps
+    (4300, 4100, 2304, "f32"), (100, 200, 9000, "bf16")])      # and a split contraction
+def test_products_by_every_tile(m, n, k, dt):
+    say("sampled", m, n, k, dt)
+    sampled_case(m, n, k, dt)
+
+
+@pytest.mark.parametrize("lens,n,k", [([2000, 1500, 0, 600], 2048, 2048), ([3000, 1, 0, 2500, 500], 2304, 2304),
+                                      ([300] * 7, 1000, 1100)])
+def test_experts_by_every_tile(lens, n, k):
+    say("sampled experts", lens, n, k)
+    sampled_case(sum(lens), n, k, "bf16", lens)
+
+
+@pytest.mark.parametrize("n", [16384, 16391])
+def test_outputs_past_the_caches(n):
+    """256 MiB of output and more, rows aligned and not."""
+    sampled_case(8200, n, 128, "bf16", dgrad=False, wgrad=False)
+
+
+def test_matrices_past_32_bits():
+    """More than 2^32 elements: codes, draws and products at the far end."""
+    m, k, n = 40000, 110016, 64
+    d = mx.linear_desc(m, n, k)
+    x = torch.empty(m, k, dtype=torch.bfloat16, device=DEV)
+    tail = rand(1, 96, k, dt="bf16")
+    for a in range(0, m, 8000):
+        x[a:a + 8000] = torch.randn(min(8000, m - a), k, device=DEV, dtype=torch.bfloat16)
+    x[m - 96:] = tail.to(DEV)
+    w = rand(2, n, k, dt="bf16")
+    wv = R.quantize(f64(w), 32)[2]
+    first = (m - 96) * k  # index of the tail's first element
+    i = np.arange(96 * k, dtype=np.uint64) + np.uint64(first)
+    with np.errstate(over="ignore"):
+        z = np.uint64(77) ^ (np.uint64(0x9E3779B97F4A7C15) * (i // np.uint64(2) + np.uint64(1)))
+        z = (z ^ (z >> np.uint64(30))) * np.uint64(0xBF58476D1CE4E5B9)
+        z = (z ^ (z >> np.uint64(27))) * np.uint64(0x94D049BB133111EB)
+        z ^= z >> np.uint64(31)
+    u = (np.where(i & np.uint64(1), z >> np.uint64(16), z >> np.uint64(40)) & np.uint64(0xFFFFFF)) / 2.0 ** 24
+    tv = R.quantize(f64(tail), 32, u.reshape(96, k))[2]
+    q = quantize(d, ACT, x, mx.MX_SR, 77)
+    for form in (0, 1):
+        mx.mx_linear_dequantize(d, ACT, q, x, form)
+        same(f64(x[m - 96:]), tv, f"form {form}")
+    y = torch.empty(m, n, device=DEV)
+    mx.mx_linear_fwd(d, quantize(d, WEIGHT, w.to(DEV)), q, y, workspace(d))
+    ref, mags = tv @ wv.T, np.abs(tv) @ np.abs(wv.T)
+    assert np.all(np.abs(f64(y[m - 96:]) - ref) <= R.bound(k, mags, ref, "f32"))
