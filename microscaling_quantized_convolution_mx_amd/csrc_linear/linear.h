@@ -172,6 +172,18 @@ bool lin_fused(const LinGeom& g);
 hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
                             void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s);
 
+// What a call launches, as the same rules choose it: for the tests, which say
+// of each case which kernel it is meant for.
+struct LinVariant {
+  int32_t kernel;  // 0: none, 1: k_lin_few, 2: k_lin_few that quantizes, 3: k_lin_product
+  int32_t size;    // stripes of a workgroup of k_lin_few, rows of a tile of k_lin_product
+  int32_t splits;  // pieces of the contraction
+  int32_t threads;
+  int64_t workgroups;
+};
+LinVariant lin_product_variant(const LinGeom& g, LinOp op);
+LinVariant lin_few_variant(const LinGeom& g, bool dgrad, bool fused);
+
 // grad_clip.hip: the list's elements are at most kMaxGradElems.
 constexpr int64_t kMaxGradElems = int64_t{1} << 43;
 size_t grad_workspace_bytes(int32_t count);

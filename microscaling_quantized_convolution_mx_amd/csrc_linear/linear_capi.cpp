@@ -240,6 +240,25 @@ mx_status mx_linear_apply(const mx_linear_desc* desc, const mx_linear_qtensor* w
                                          ws + apply_code_bytes(g) + apply_scale_bytes(g), stream));
 }
 
+// Not part of the ABI: the kernel, size, pieces, threads and workgroups of
+// linear.h's LinVariant for mx_linear_fwd (0), _dgrad (1), _wgrad (2) or
+// _apply's product (3) on this descriptor.  Launches nothing.
+mx_status mx_internal_linear_variant(const mx_linear_desc* desc, int call, int64_t* out) {
+  const mx_status st = check_desc(desc);
+  if (st != MX_OK) return st;
+  if (!out) return MX_ERR_NULL;
+  const LinGeom g = mx::make_lin_geom(desc);
+  const mx::LinVariant v = call == 3 && g.m > 0 && mx::lin_fused(g)
+                               ? mx::lin_few_variant(g, false, true)
+                               : mx::lin_product_variant(g, call == 1 ? mx::LIN_DGRAD : call == 2 ? mx::LIN_WGRAD : mx::LIN_FWD);
+  out[0] = v.kernel;
+  out[1] = v.size;
+  out[2] = v.splits;
+  out[3] = v.threads;
+  out[4] = v.workgroups;
+  return MX_OK;
+}
+
 size_t mx_grad_workspace_bytes(int32_t count) { return count > 0 ? mx::grad_workspace_bytes(count) : 0; }
 
 mx_status mx_grad_norm(const mx_grad_list* list, float* norm, void* workspace, size_t ws_bytes, hipStream_t stream) {

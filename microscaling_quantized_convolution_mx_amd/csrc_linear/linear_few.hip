@@ -253,7 +253,18 @@ FewParams make_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, vo
   return p;
 }
 
+LinVariant variant(const FewParams& p, int sn, bool fused) {
+  return {fused ? 2 : 1, sn, 1, 64 * waves_of(p.kt), static_cast<int64_t>(p.per_xcd) * 8};
+}
+
 }  // namespace
+
+LinVariant lin_few_variant(const LinGeom& g, bool dgrad, bool fused) {
+  const mx_linear_qtensor none{};
+  int sn;
+  const FewParams p = make_few(g, dgrad, &none, nullptr, MX_F32, 0, nullptr, sn);
+  return variant(p, sn, fused);
+}
 
 // Quantizing M tokens in every group of stripes takes about
 // M * columns * groups / 2e12 s over the whole GPU, much of it while the weight
@@ -282,7 +293,8 @@ hipError_t launch_lin_fused(const LinGeom& g, const mx_linear_qtensor* wq, const
   const int waves = waves_of(p.kt), most = tokens_per_pass(p.kt);
   p.per_pass = g.m < most ? static_cast<int>(g.m) : most;
   const size_t lds = fused_lds(p.kt, waves, p.per_pass);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
+  const LinVariant v = variant(p, sn, true);
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(v.workgroups)), dim3(v.threads), lds, s, p); };
   auto with = [&](auto t) {
     using T = decltype(t);
     sn == 4 ? go(k_lin_few<T, 4>) : sn == 2 ? go(k_lin_few<T, 2>) : go(k_lin_few<T, 1>);
@@ -304,7 +316,8 @@ hipError_t launch_lin_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor*
   const int waves = waves_of(p.kt);
   const int64_t tokens = g.m < 32 ? g.m : 32;
   const size_t lds = static_cast<size_t>(waves) * tokens * kSumStride * 4;
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(p.per_xcd) * 8), dim3(64 * waves), lds, s, p); };
+  const LinVariant v = variant(p, sn, false);
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(v.workgroups)), dim3(v.threads), lds, s, p); };
   sn == 4 ? go(k_lin_few<void, 4>) : sn == 2 ? go(k_lin_few<void, 2>) : go(k_lin_few<void, 1>);
   return hipGetLastError();
 }

@@ -480,7 +480,19 @@ Plan make_plan(const LinGeom& g, LinOp op) {
   return best;
 }
 
+LinVariant variant(const Plan& pl) {
+  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny::TM;
+  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : Tiny::kThreads;
+  return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
+}
+
 }  // namespace
+
+LinVariant lin_product_variant(const LinGeom& g, LinOp op) {
+  if (op != LIN_WGRAD && g.m == 0) return {};
+  if (op != LIN_WGRAD && lin_few(g)) return lin_few_variant(g, op == LIN_DGRAD, false);
+  return variant(make_plan(g, op));
+}
 
 size_t lin_product_workspace(const LinGeom& g, LinOp op) {
   if (g.m == 0 || (op != LIN_WGRAD && lin_few(g))) return 0;
@@ -532,14 +544,13 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.tiles_j = static_cast<int>(pl.tiles_j);
   p.splits = pl.splits;
   p.split_steps = pl.split_steps;
-  const unsigned grid = static_cast<unsigned>((pl.units * pl.splits + 7) / 8 * 8);
+  const LinVariant v = variant(pl);
   auto multiply = [&](auto t) {
     using T = decltype(t);
-    auto launch = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), 0, s, p); };
+    auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(v.workgroups)), dim3(v.threads), 0, s, p); };
     auto with = [&](auto contract) {
       constexpr bool C = decltype(contract)::value;
-      pl.shape == 2 ? launch(k_lin_product<T, Big, C>, Big::kThreads)
-                    : pl.shape == 1 ? launch(k_lin_product<T, Small, C>, Small::kThreads) : launch(k_lin_product<T, Tiny, C>, Tiny::kThreads);
+      pl.shape == 2 ? launch(k_lin_product<T, Big, C>) : pl.shape == 1 ? launch(k_lin_product<T, Small, C>) : launch(k_lin_product<T, Tiny, C>);
     };
     op == LIN_WGRAD ? with(std::true_type{}) : with(std::false_type{});
   };

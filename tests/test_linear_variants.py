@@ -1,0 +1,64 @@
+"""Which kernel a call takes (on the host): the cases of the GPU tests reach
+every variant of the products and of the few-token kernel."""
+import pytest
+
+import linear_variants as V
+import microscaling_quantized_convolution_mx_amd as mx
+from linear_variants import variant
+
+
+def describe(c):
+    m, n, k, lens = c
+    assert lens is None or sum(lens) == m
+    return mx.linear_desc(m, n, k, experts=len(lens or ()))
+
+
+@pytest.mark.parametrize("case", V.PRODUCTS, ids=lambda c: f"{c[0][:3]}")
+def test_products_take_the_tile_that_the_case_is_for(case):
+    d = describe(case[0])
+    for call, want in enumerate(case[1:]):
+        v = variant(d, call)
+        assert (v.kernel, v.size, v.splits > 1) == (V.PRODUCT, *want), call
+        assert mx.mx_linear_workspace_bytes(d) > 0 or v.splits == 1
+
+
+@pytest.mark.parametrize("case", V.FEW_TOKENS, ids=lambda c: f"{c[0][:3]}")
+def test_few_tokens_take_the_stripes_that_the_case_is_for(case):
+    d = describe(case[0])
+    for call, want in ((V.FWD, case[1]), (V.DGRAD, case[2])):
+        v = variant(d, call)
+        assert (v.kernel, v.size) == (V.FEW, want), call
+    v = variant(d, V.APPLY)
+    assert (v.size, v.kernel) == (case[3][0], V.FUSED if case[3][1] else V.FEW)
+
+
+def test_the_cases_reach_every_variant():
+    product = {(call, *w, c[0][3] is not None) for c in V.PRODUCTS for call, w in enumerate(c[1:])}
+    for call in (V.FWD, V.DGRAD, V.WGRAD):
+        for size in (64, 128, 256):
+            assert (call, size, False, False) in product and (call, size, False, True) in product
+        assert (call, 64, True, False) in product
+    for experts in (False, True):
+        few = [c for c in V.FEW_TOKENS if (c[0][3] is not None) == experts]
+        for stripes in (2, 4) if experts else (1, 2, 4):
+            assert any(stripes in c[1:3] for c in few)
+            assert any(c[3] == (stripes, True) for c in few)
+
+
+def test_no_tokens():
+    d = mx.linear_desc(0, 70, 200)
+    assert [variant(d, c).kernel for c in (V.FWD, V.DGRAD, V.WGRAD, V.APPLY)] == [V.NONE, V.NONE, V.PRODUCT, V.NONE]
+
+
+@pytest.mark.parametrize("call,shape", [(V.FWD, (203, 130, 4100)), (V.DGRAD, (203, 4100, 130)), (V.WGRAD, (4097, 65, 67))])
+def test_every_split_product_refuses_a_short_workspace(call, shape):
+    m, n, k = shape
+    d = mx.linear_desc(m, n, k)
+    v = variant(d, call)
+    rows, cols = ((m, n), (m, k), (n, k))[call]
+    need = v.splits * rows * ((cols + 3) // 4 * 4) * 4
+    q = mx.mx_linear_qtensor(*(0x10000,) * 4)
+    f = getattr(mx.lib(), ("mx_linear_fwd", "mx_linear_dgrad", "mx_linear_wgrad")[call])
+    for ws, n_bytes in ((None, need), (0x10000, need - 1), (0x10000, 0)):
+        assert f(d, q, q, 0x10000, 0, cols, None, ws, n_bytes, None) == -6
+    assert mx.mx_linear_workspace_bytes(d) >= need
