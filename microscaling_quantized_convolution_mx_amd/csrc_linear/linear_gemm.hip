@@ -20,6 +20,7 @@
 #include "internal.h"
 #include "linear.h"
 
+#include <limits>
 #include <type_traits>
 #include <utility>
 
@@ -433,6 +434,12 @@ struct Plan {
   int64_t units;  // workgroups, at most
 };
 
+LinVariant variant(const Plan& pl) {
+  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny::TM;
+  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : Tiny::kThreads;
+  return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
+}
+
 // Tiles and split by estimated time, in us, fitted to measured products (bf16
 // outputs, 64 to 8192 rows and 512 to 8192 columns).  A round is 256
 // workgroups, one per CU:
@@ -444,7 +451,9 @@ struct Plan {
 //          (777x1000x520 4.6, Small 7.4; 301x2500x1999 6.3, Small 9.3)
 // Splitting the contraction costs a launch, 3, and the traffic of its partial
 // sums at 4 TB/s: it pays for long contractions with few outputs, seldom else
-// (512x4096x4096 by Small 12.7, in 2 pieces 18.3).
+// (512x4096x4096 by Small 12.7, in 2 pieces 18.3).  Tiles too small for a
+// launch's 2^32 - 1 threads are left out (a contraction of length 0 over 2^36
+// outputs would take Tiny): check_desc keeps Small and Big below that.
 Plan make_plan(const LinGeom& g, LinOp op) {
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
   const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
@@ -469,6 +478,8 @@ Plan make_plan(const LinGeom& g, LinOp op) {
     const double rounds = static_cast<double>((likely * pl.splits + 255) / 256), each = steps / pl.splits;
     double time = shape == 2 ? rounds * (9.0 + 0.8 * each) : shape == 1 ? 5.0 + rounds * 0.28 * each : 3.6 + rounds * 0.13 * each;
     if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
+    const LinVariant v = variant(pl);
+    if (v.workgroups * v.threads > std::numeric_limits<uint32_t>::max()) return;
     if (best.units == 0 || time < best_time) {
       best = pl;
       best_time = time;
@@ -478,12 +489,6 @@ Plan make_plan(const LinGeom& g, LinOp op) {
   if (g.e == 0)
     for (int64_t s = 2; s <= 16 && 4 * s <= all_steps; s *= 2) consider(0, s);
   return best;
-}
-
-LinVariant variant(const Plan& pl) {
-  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny::TM;
-  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : Tiny::kThreads;
-  return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
 }
 
 }  // namespace

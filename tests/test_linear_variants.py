@@ -62,3 +62,16 @@ def test_every_split_product_refuses_a_short_workspace(call, shape):
     for ws, n_bytes in ((None, need), (0x10000, need - 1), (0x10000, 0)):
         assert f(d, q, q, 0x10000, 0, cols, None, ws, n_bytes, None) == -6
     assert mx.mx_linear_workspace_bytes(d) >= need
+
+
+@pytest.mark.parametrize("shape", [
+    (0, 8192, 8192, 1024), (1, 8192, 8192, 1024), (2 ** 20, 8192, 8192, 1024), (0, 2 ** 18, 2 ** 18, 0), (33, 2 ** 18, 2 ** 18, 0),
+    (2 ** 30 - 200, 100, 100, 0), (2 ** 30 - 2 ** 18, 100, 100, 1024), (2 ** 23, 16000, 16000, 0), (2, 2 ** 30 - 200, 100, 0),
+    (2, 100, 2 ** 30 - 200, 0), (16384, 2 ** 19, 100, 1023), (100, 1, 2 ** 19, 1023)])
+def test_every_launch_fits_the_threads_of_one(shape):
+    """2^32 - 1 threads, also where the contraction is empty and the output large."""
+    m, n, k, e = shape
+    d = mx.linear_desc(m, n, k, experts=e)
+    for call in (V.FWD, V.DGRAD, V.WGRAD, V.APPLY):
+        v = variant(d, call)
+        assert v.workgroups * v.threads < 2 ** 32, (call, v)
