@@ -188,7 +188,7 @@ unsigned groups(const Batch& b) {
 }  // namespace
 
 size_t grad_workspace_bytes(int32_t count) {
-  return static_cast<size_t>((count + kTensors - 1) / kTensors) * kMaxGroups * sizeof(double);
+  return (static_cast<size_t>(count) + kTensors - 1) / kTensors * kMaxGroups * sizeof(double);
 }
 
 hipError_t launch_grad_clip(const mx_grad_list* l, bool clip, float max_norm, float* norm, void* workspace, hipStream_t s) {
