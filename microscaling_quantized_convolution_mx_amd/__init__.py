@@ -167,13 +167,47 @@ def _buf(t, need: int, what: str, fp32: bool = True) -> int | None:
     return t.data_ptr() if t.numel() > 0 else None
 
 
-def _stream(stream) -> int | None:
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
+def _index(t) -> int | None:
+    """Index of a tensor's device; raw addresses and None have none."""
+    return None if t is None or isinstance(t, int) else t.get_device()
+
+
+_current_device = _current_stream = None
+
+
+def _bind_torch() -> None:
+    """torch's current device, and the current stream's handle on a device."""
+    global _current_device, _current_stream
     import torch
+    _current_device = torch.cuda.current_device
     # the handle alone, where torch has it: building a Stream object takes longer than a launch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _stream(stream, *devices) -> int | None:
+    """The handle of the stream that a call goes to (None: the current one),
+    after checking that everything the call was given lies on that stream's
+    device: a kernel that reads another GPU's memory would fault.  devices: the
+    indexes of the tensors' devices, None for what has none (raw addresses, no
+    tensor).  Of a raw handle other than 0 only its caller knows the device;
+    the tensors then have to share one."""
+    if _current_device is None:
+        _bind_torch()
+    dev = None
+    if stream is None:
+        dev = _current_device()
+        handle = _current_stream(dev)
+    elif isinstance(stream, int):
+        handle = stream
+    else:
+        handle, dev = stream.cuda_stream, getattr(stream, "device_index", None)
+    for at in devices:
+        if at is not None and at != dev:
+            if dev is None:
+                dev = at if handle else _current_device()
+            if at != dev:
+                raise ValueError(f"a tensor in the memory of device {at}, the call runs on device {dev}")
+    return handle
 
 
 def _check(status: int, where: str) -> None:

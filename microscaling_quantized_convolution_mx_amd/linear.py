@@ -98,12 +98,20 @@ def _dims(d: mx_linear_desc, role: int):
     return d.tokens, (d.out_features if role == _mx.MX_ROLE_GRAD else d.in_features)
 
 
+def _device(t, what: str) -> int:
+    """Index of the device whose memory holds t."""
+    at = t.get_device()
+    if at < 0 and not t.is_cuda:
+        raise ValueError(f"{what}: must be in device memory, got a {t.device.type} tensor")
+    return at
+
+
 def _matrix(t, shape, what: str):
-    """(address, mx_dtype, row stride) of a tensor after checking it: nothing
-    that the kernels could not read reaches them.  None passes through as a
-    NULL float32 matrix (the library reports MX_ERR_NULL)."""
+    """(address, mx_dtype, row stride, device) of a tensor after checking it:
+    nothing that the kernels could not read reaches them.  None passes through
+    as a NULL float32 matrix (the library reports MX_ERR_NULL)."""
     if t is None:
-        return None, MX_F32, shape[-1]
+        return None, MX_F32, shape[-1], None
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{what}: expected a torch tensor, got {type(t).__name__}")
     dt = _dtypes.get(t.dtype)
@@ -111,10 +119,9 @@ def _matrix(t, shape, what: str):
         raise ValueError(f"{what}: must be float32, bfloat16 or float16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be in device memory, got a {t.device.type} tensor")
+    at = _device(t, what)
     if t.is_contiguous():
-        return t.data_ptr() or None, dt, shape[-1]
+        return t.data_ptr() or None, dt, shape[-1], at
     st = t.stride()
     rows, cols = shape[-2], shape[-1]
     if st[-1] != 1 and cols > 1:
@@ -126,30 +133,29 @@ def _matrix(t, shape, what: str):
             raise ValueError(f"{what}: experts must follow each other without a gap")
     if ld < cols:
         raise ValueError(f"{what}: rows overlap (row stride {ld}, {cols} columns)")
-    return t.data_ptr() or None, dt, ld
+    return t.data_ptr() or None, dt, ld, at
 
 
 def _offsets(d: mx_linear_desc, t):
+    """(address, device) of the experts' offsets."""
     if d.experts <= 0 or t is None:
-        return None
+        return None, None
     if not isinstance(t, _torch.Tensor) or t.dtype != _torch.int32 or not t.is_contiguous():
         raise ValueError("offsets: must be a contiguous int32 tensor")
     if t.numel() != d.experts + 1:
         raise ValueError(f"offsets: {t.numel()} values, the call needs {d.experts + 1}")
-    if not t.is_cuda:
-        raise ValueError(f"offsets: must be in device memory, got a {t.device.type} tensor")
-    return t.data_ptr()
+    at = _device(t, "offsets")
+    return t.data_ptr(), at
 
 
 def _bytes(t, what: str):
-    """(address, bytes) of a workspace tensor of any type."""
+    """(address, bytes, device) of a workspace tensor of any type."""
     if t is None:
-        return None, 0
+        return None, 0, None
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be in device memory, got a {t.device.type} tensor")
-    return t.data_ptr() or None, t.numel() * t.element_size()
+    at = _device(t, what)
+    return t.data_ptr() or None, t.numel() * t.element_size(), at
 
 
 def mx_linear_code_bytes(d: mx_linear_desc, role: int, form: int = MX_FORM_ROWS) -> int:
@@ -180,6 +186,7 @@ class LinearQTensor:
                 self.bytes[form] = n
                 self.buffers[form] = tuple(torch.empty(max(b, 16), dtype=torch.uint8, device=device) for b in n)
         self.is_cuda = all(b.is_cuda for f in self.buffers.values() for b in f)
+        self.device_index = next((b.get_device() for f in self.buffers.values() for b in f), None)
         none = (None, None)
         self.c = mx_linear_qtensor(*(b.data_ptr() if b is not None else None
                                      for form in (MX_FORM_ROWS, MX_FORM_COLS) for b in self.buffers.get(form, none)))
@@ -205,6 +212,11 @@ def _q(q, d: mx_linear_desc, role: int, forms, what: str):
     return q.c
 
 
+def _index(q):
+    """Device index of a LinearQTensor; raw addresses have none."""
+    return q.device_index if isinstance(q, LinearQTensor) else None
+
+
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise _mx.MxError(status, where)
@@ -214,26 +226,29 @@ def mx_linear_quantize(d: mx_linear_desc, role: int, src, dst, rounding: int = 0
                        stream=None) -> None:
     """Fills the forms that dst has."""
     L = _load()
-    p, dt, ld = _matrix(src, _dims(d, role), "src")
+    p, dt, ld, at = _matrix(src, _dims(d, role), "src")
     q = _q(dst, d, role, dst.bytes if isinstance(dst, LinearQTensor) else (), "dst")
-    _check(L.mx_linear_quantize(d, role, p, dt, ld, _offsets(d, offsets), q, rounding, seed & (2 ** 64 - 1),
-                                _mx._stream(stream)), "mx_linear_quantize")
+    off, oat = _offsets(d, offsets)
+    _check(L.mx_linear_quantize(d, role, p, dt, ld, off, q, rounding, seed & (2 ** 64 - 1),
+                                _mx._stream(stream, at, _index(dst), oat)), "mx_linear_quantize")
 
 
 def mx_linear_dequantize(d: mx_linear_desc, role: int, q, dst, form: int = MX_FORM_ROWS, offsets=None, stream=None) -> None:
     L = _load()
-    p, dt, ld = _matrix(dst, _dims(d, role), "dst")
-    _check(L.mx_linear_dequantize(d, role, form, _q(q, d, role, (form,), "q"), p, dt, ld, _offsets(d, offsets),
-                                  _mx._stream(stream)), "mx_linear_dequantize")
+    p, dt, ld, at = _matrix(dst, _dims(d, role), "dst")
+    off, oat = _offsets(d, offsets)
+    _check(L.mx_linear_dequantize(d, role, form, _q(q, d, role, (form,), "q"), p, dt, ld, off,
+                                  _mx._stream(stream, at, _index(q), oat)), "mx_linear_dequantize")
 
 
 def _product(name, d, q1, role1, form1, q2, role2, form2, out, role, what, workspace, offsets, stream):
     L = _load()
-    p, dt, ld = _matrix(out, _dims(d, role), what)
-    ws, n = _bytes(workspace, "workspace")
+    p, dt, ld, at = _matrix(out, _dims(d, role), what)
+    ws, n, wat = _bytes(workspace, "workspace")
+    off, oat = _offsets(d, offsets)
     a = _q(q1, d, role1, (form1,), "wq" if role1 == _mx.MX_ROLE_WEIGHT else "dyq")
     b = _q(q2, d, role2, (form2,), "xq" if role2 == _mx.MX_ROLE_ACT else "dyq")
-    _check(getattr(L, name)(d, a, b, p, dt, ld, _offsets(d, offsets), ws, n, _mx._stream(stream)), name)
+    _check(getattr(L, name)(d, a, b, p, dt, ld, off, ws, n, _mx._stream(stream, at, _index(q1), _index(q2), wat, oat)), name)
 
 
 def mx_linear_fwd(d: mx_linear_desc, wq, xq, y, workspace=None, offsets=None, stream=None) -> None:
@@ -257,11 +272,12 @@ def mx_linear_wgrad(d: mx_linear_desc, dyq, xq, dw, workspace=None, offsets=None
 def mx_linear_apply(d: mx_linear_desc, wq, x, y, workspace=None, offsets=None, stream=None) -> None:
     """Y = X W^T with X quantized on the way (1x32 blocks)."""
     L = _load()
-    px, dx, ldx = _matrix(x, (d.tokens, d.in_features), "x")
-    py, dy, ldy = _matrix(y, (d.tokens, d.out_features), "y")
-    ws, n = _bytes(workspace, "workspace")
+    px, dx, ldx, xat = _matrix(x, (d.tokens, d.in_features), "x")
+    py, dy, ldy, yat = _matrix(y, (d.tokens, d.out_features), "y")
+    ws, n, wat = _bytes(workspace, "workspace")
+    off, oat = _offsets(d, offsets)
     _check(L.mx_linear_apply(d, _q(wq, d, _mx.MX_ROLE_WEIGHT, (MX_FORM_ROWS,), "wq"), px, dx, ldx, py, dy, ldy,
-                             _offsets(d, offsets), ws, n, _mx._stream(stream)), "mx_linear_apply")
+                             off, ws, n, _mx._stream(stream, xat, yat, _index(wq), wat, oat)), "mx_linear_apply")
 
 
 class GradList:
@@ -288,6 +304,10 @@ class GradList:
                     raise ValueError(f"{what} {i}: must be in device memory, got a {t.device.type} tensor")
             if g.dtype != o.dtype or g.numel() != o.numel():
                 raise ValueError(f"output {i}: must have its gradient's type and size")
+        at = {t.get_device() for t in (*self.grads, *self.out)}
+        if len(at) > 1:
+            raise ValueError(f"gradients and outputs on devices {sorted(at)}, one list is of one device")
+        self.device_index = at.pop() if at else None
         n = max(len(self.grads), 1)
         self._a = ((ctypes.c_void_p * n)(*(g.data_ptr() or None for g in self.grads)),
                    (ctypes.c_void_p * n)(*(o.data_ptr() or None for o in self.out)),
@@ -306,12 +326,14 @@ def mx_grad_workspace_bytes(grads) -> int:
 
 def mx_grad_norm(grads: GradList, norm, workspace=None, stream=None) -> None:
     """norm[0] = the norm over all gradients."""
-    ws, n = _bytes(workspace, "workspace")
-    _check(_load().mx_grad_norm(grads.c, _mx._buf(norm, 4, "norm"), ws, n, _mx._stream(stream)), "mx_grad_norm")
+    ws, n, at = _bytes(workspace, "workspace")
+    _check(_load().mx_grad_norm(grads.c, _mx._buf(norm, 4, "norm"), ws, n,
+                                _mx._stream(stream, grads.device_index, at, _mx._index(norm))), "mx_grad_norm")
 
 
 def mx_grad_clip(grads: GradList, max_norm: float, norm, workspace=None, stream=None) -> None:
     """norm[0] = the norm over all gradients, which are then scaled by
     min(1, max_norm / (norm + 1e-6)) into their outputs."""
-    ws, n = _bytes(workspace, "workspace")
-    _check(_load().mx_grad_clip(grads.c, max_norm, _mx._buf(norm, 4, "norm"), ws, n, _mx._stream(stream)), "mx_grad_clip")
+    ws, n, at = _bytes(workspace, "workspace")
+    _check(_load().mx_grad_clip(grads.c, max_norm, _mx._buf(norm, 4, "norm"), ws, n,
+                                _mx._stream(stream, grads.device_index, at, _mx._index(norm))), "mx_grad_clip")
