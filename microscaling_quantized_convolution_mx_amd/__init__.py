@@ -271,17 +271,26 @@ def _q(q, d: mx_conv_desc | None = None, role: int | None = None, what: str = "q
     raise TypeError(f"{what}: expected a QTensor or an mx_qtensor, got {type(q).__name__}")
 
 
+def _indexes(*held):
+    """Device indexes of the tensors among `held`, a QTensor's four among them."""
+    for t in held:
+        if isinstance(t, QTensor):
+            yield from (b.get_device() for b in (t.codes, t.scales, t.tensor_scale, t.amax))
+        elif not isinstance(t, mx_qtensor):
+            yield _index(t)
+
+
 def mx_quantize_cbf(d: mx_conv_desc, role: int, src, dst, rounding: int = MX_RNE, seed: int = 0,
                     amax_given: bool = False, stream=None) -> None:
     args = (ctypes.byref(d), role, _buf(src, 4 * role_numel(d, role), "src"), _q(dst, d, role, "dst"), rounding,
             seed & (2 ** 64 - 1), int(bool(amax_given)))
-    _check(lib().mx_quantize_cbf(*args, _stream(stream)), "mx_quantize_cbf")
+    _check(lib().mx_quantize_cbf(*args, _stream(stream, *_indexes(src, dst))), "mx_quantize_cbf")
 
 
 def mx_conv_fwd(d: mx_conv_desc, wq, xq, y, stream=None) -> None:
     args = (ctypes.byref(d), _q(wq, d, MX_ROLE_WEIGHT, "wq"), _q(xq, d, MX_ROLE_ACT, "xq"),
             _buf(y, 4 * role_numel(d, MX_ROLE_GRAD), "y"))
-    _check(lib().mx_conv_fwd(*args, _stream(stream)), "mx_conv_fwd")
+    _check(lib().mx_conv_fwd(*args, _stream(stream, *_indexes(wq, xq, y))), "mx_conv_fwd")
 
 
 def mx_fwd_amax_bytes(d: mx_conv_desc) -> int:
@@ -291,13 +300,13 @@ def mx_fwd_amax_bytes(d: mx_conv_desc) -> int:
 def mx_conv_fwd_amax(d: mx_conv_desc, wq, xq, y, y_amax, stream=None) -> None:
     args = (ctypes.byref(d), _q(wq, d, MX_ROLE_WEIGHT, "wq"), _q(xq, d, MX_ROLE_ACT, "xq"),
             _buf(y, 4 * role_numel(d, MX_ROLE_GRAD), "y"), _buf(y_amax, mx_fwd_amax_bytes(d), "y_amax", fp32=False))
-    _check(lib().mx_conv_fwd_amax(*args, _stream(stream)), "mx_conv_fwd_amax")
+    _check(lib().mx_conv_fwd_amax(*args, _stream(stream, *_indexes(wq, xq, y, y_amax))), "mx_conv_fwd_amax")
 
 
 def mx_conv_dgrad(d: mx_conv_desc, wq, dyq, dx, stream=None) -> None:
     args = (ctypes.byref(d), _q(wq, d, MX_ROLE_WEIGHT, "wq"), _q(dyq, d, MX_ROLE_GRAD, "dyq"),
             _buf(dx, 4 * role_numel(d, MX_ROLE_ACT), "dx"))
-    _check(lib().mx_conv_dgrad(*args, _stream(stream)), "mx_conv_dgrad")
+    _check(lib().mx_conv_dgrad(*args, _stream(stream, *_indexes(wq, dyq, dx))), "mx_conv_dgrad")
 
 
 def mx_conv_wgrad(d: mx_conv_desc, dyq, xq, dw, workspace, ws_bytes: int | None = None,
@@ -308,7 +317,7 @@ def mx_conv_wgrad(d: mx_conv_desc, dyq, xq, dw, workspace, ws_bytes: int | None 
     args = (ctypes.byref(d), _q(dyq, d, MX_ROLE_GRAD, "dyq"), _q(xq, d, MX_ROLE_ACT, "xq"),
             _buf(dw, 4 * role_numel(d, MX_ROLE_WEIGHT), "dw"), _buf(workspace, ws_bytes, "workspace", fp32=False),
             ws_bytes)
-    _check(lib().mx_conv_wgrad(*args, _stream(stream)), "mx_conv_wgrad")
+    _check(lib().mx_conv_wgrad(*args, _stream(stream, *_indexes(dyq, xq, dw, workspace))), "mx_conv_wgrad")
 
 
 def mx_conv_wgrad_noalloc(d: mx_conv_desc, dyq, xq, dw, stream=None) -> None:
@@ -316,18 +325,18 @@ def mx_conv_wgrad_noalloc(d: mx_conv_desc, dyq, xq, dw, stream=None) -> None:
     that cannot allocate); calls that overlap in time on one GPU race."""
     args = (ctypes.byref(d), _q(dyq, d, MX_ROLE_GRAD, "dyq"), _q(xq, d, MX_ROLE_ACT, "xq"),
             _buf(dw, 4 * role_numel(d, MX_ROLE_WEIGHT), "dw"))
-    _check(lib().mx_conv_wgrad_noalloc(*args, _stream(stream)), "mx_conv_wgrad_noalloc")
+    _check(lib().mx_conv_wgrad_noalloc(*args, _stream(stream, *_indexes(dyq, xq, dw))), "mx_conv_wgrad_noalloc")
 
 
 def mx_im2col_cbf(d: mx_conv_desc, x, xcol, stream=None) -> None:
     ncol = max(d.h_out, 0) * max(d.w_out, 0) * d.k_h * d.k_w * d.c_in * d.n
     args = (ctypes.byref(d), _buf(x, 4 * role_numel(d, MX_ROLE_ACT), "x"), _buf(xcol, 4 * ncol, "xcol"))
-    _check(lib().mx_im2col_cbf(*args, _stream(stream)), "mx_im2col_cbf")
+    _check(lib().mx_im2col_cbf(*args, _stream(stream, *_indexes(x, xcol))), "mx_im2col_cbf")
 
 
 def mx_dequantize(d: mx_conv_desc, role: int, q, dst, stream=None) -> None:
     args = (ctypes.byref(d), role, _q(q, d, role, "q"), _buf(dst, 4 * role_numel(d, role), "dst"))
-    _check(lib().mx_dequantize(*args, _stream(stream)), "mx_dequantize")
+    _check(lib().mx_dequantize(*args, _stream(stream, *_indexes(q, dst))), "mx_dequantize")
 
 
 # The microscaled linear layers and the gradient clip (include/mxlinear.h).
