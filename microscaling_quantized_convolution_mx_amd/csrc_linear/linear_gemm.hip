@@ -138,14 +138,16 @@ __device__ __forceinline__ void store_wave(const f32x16 (&acc)[RM][RN], uint8_t*
 // does not know of the copy (told of it, it would wait for all copies on
 // their way before any LDS read), so whoever reads the data waits for it with
 // wait_barrier.  There is no output register, and the address registers are
-// read when the instruction issues.
+// read when the instruction issues.  The LDS address goes in m0, which is an
+// operand, so that the compiler writes it and knows of it (and an instruction
+// has to pass between that write and the copy).
 template <int BYTES>
 __device__ __forceinline__ void copy_lds(const uint8_t* src, uint32_t dst, int lane) {
   const uint32_t off = static_cast<uint32_t>(lane) * BYTES;
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(dst), "v"(off), "s"(src) : "m0", "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "{m0}"(dst), "v"(off), "s"(src) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(dst), "v"(off), "s"(src) : "m0", "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" : : "{m0}"(dst), "v"(off), "s"(src) : "memory");
 }
 
 // Waits until at most N of the wave's copies and none of its LDS reads are on
