@@ -54,4 +54,6 @@ FEW_TOKENS = [
     ((64, 1030, 300, [1, 0, 7, 0] * 4 + [0] * 47 + [32]), 4, 2, (4, True)),
     ((300, 900, 1000, [40, 0, 1, 100] + [9] * 15 + [24]), 2, 2, (2, True)),
     ((1000, 1030, 2100, [70, 0, 1] + [15] * 60 + [29]), 4, 4, (4, False)),
+    ((999, 300, 260, [0] * 40 + [999] + [0] * 23), 2, 2, (2, True)),
+    ((301, 300, 260, [301] + [0] * 39), 1, 1, (1, True)),
 ]

@@ -75,3 +75,16 @@ def test_every_launch_fits_the_threads_of_one(shape):
     for call in (V.FWD, V.DGRAD, V.WGRAD, V.APPLY):
         v = variant(d, call)
         assert v.workgroups * v.threads < 2 ** 32, (call, v)
+
+
+@pytest.mark.parametrize("m,n,k,e", [(1024, 2048, 2048, 64), (16384, 512, 512, 1024), (301, 300, 260, 40), (16, 2048, 1024, 64)])
+def test_few_tokens_of_one_expert_are_not_walked_one_after_the_other(m, n, k, e):
+    """Whatever the routing, each 32 tokens of an expert and each group of its weight's stripes have a workgroup."""
+    d = mx.linear_desc(m, n, k, experts=e)
+    for call, lines in ((V.FWD, n), (V.DGRAD, k), (V.APPLY, n)):
+        v = variant(d, call)
+        assert v.kernel in (V.FEW, V.FUSED)
+        stripes = (lines + 31) // 32
+        for used in (1, min(m, e)):
+            passes = used - 1 + (m - used + 1 + 31) // 32
+            assert v.workgroups >= passes * ((stripes + v.size - 1) // v.size)
