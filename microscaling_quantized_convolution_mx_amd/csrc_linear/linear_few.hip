@@ -276,17 +276,17 @@ LinVariant lin_few_variant(const LinGeom& g, bool dgrad, bool fused) {
   return variant(p, sn, fused);
 }
 
-// Quantizing M tokens in every group of stripes takes about
+// Quantizing M tokens in every group of an expert's stripes takes about
 // M * columns * groups / 2e12 s over the whole GPU, much of it while the weight
 // is on its way; a launch of its own takes about 4 us and an L2 read of the
-// codes.  (In graphs: 256 tokens of 64 experts, 2048x2048, 8.9M elements, 24 us here
+// codes.  (In graphs: 256 tokens of 64 experts, 2048x2048, 8.4M elements, 24 us here
 // and 31 in two launches; 16x8192x2048, 8.4M, 5.7 and 6.5; 32x8192x2048, 16.8M, 7.9
 // and 6.9.)
 bool lin_fused(const LinGeom& g) {
-  const int64_t kt = g.kp / kTileC, stripes = (g.n + kTileR - 1) / kTileR * g.ew;
-  const int t = tokens_per_pass(kt);
-  const int64_t groups = stripes / stripes_per_group(stripes) / g.ew + 1;
-  if (t == 0 || g.m * g.kp * groups > (int64_t{1} << 24)) return false;
+  const int64_t kt = g.kp / kTileC, stripes = (g.n + kTileR - 1) / kTileR;
+  const int t = tokens_per_pass(kt), sn = stripes_per_group(stripes * g.ew);
+  const int64_t groups = (stripes + sn - 1) / sn;
+  if (t == 0 || g.m * g.kp * groups >= (int64_t{1} << 24)) return false;
   return g.e == 0 ? g.m <= t : lin_few(g);
 }
 

@@ -88,3 +88,16 @@ def test_few_tokens_of_one_expert_are_not_walked_one_after_the_other(m, n, k, e)
         for used in (1, min(m, e)):
             passes = used - 1 + (m - used + 1 + 31) // 32
             assert v.workgroups >= passes * ((stripes + v.size - 1) // v.size)
+
+
+@pytest.mark.parametrize("m,n,k,e,fused", [
+    (32, 8192, 2048, 0, False), (31, 8192, 2048, 0, True),             # 256 groups of one stripe
+    (32, 8191, 2048, 0, False), (32, 8160, 2048, 0, True),             # 256 and 255
+    (31, 16400, 1024, 0, True), (31, 16385, 1920, 0, True), (32, 16352, 2048, 0, False),  # 257, 257 and 256 of two
+    (1023, 2048, 1024, 64, True), (1024, 2048, 1024, 64, False)])      # 16 groups of four in each expert
+def test_tokens_are_quantized_on_the_way_below_2_24_elements(m, n, k, e, fused):
+    """Tokens x padded features x groups of stripes of one expert, those that the launch has."""
+    v = variant(mx.linear_desc(m, n, k, experts=e), V.APPLY)
+    assert v.kernel == (V.FUSED if fused else V.FEW)
+    groups = -(-(-(-n // 32)) // v.size)
+    assert (m * -(-k // 128) * 128 * groups < 2 ** 24) == fused
