@@ -183,6 +183,7 @@ struct LinVariant {
 };
 LinVariant lin_product_variant(const LinGeom& g, LinOp op);
 LinVariant lin_few_variant(const LinGeom& g, bool dgrad, bool fused);
+bool lin_product_streams(const LinGeom& g, LinOp op, const void* out, mx_dtype dtype, int64_t ld);
 
 // grad_clip.hip: the list's elements are at most kMaxGradElems.
 constexpr int64_t kMaxGradElems = int64_t{1} << 43;

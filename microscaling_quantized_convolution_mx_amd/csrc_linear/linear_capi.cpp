@@ -259,6 +259,13 @@ mx_status mx_internal_linear_variant(const mx_linear_desc* desc, int call, int64
   return MX_OK;
 }
 
+// Not part of the ABI: whether mx_linear_fwd (0), _dgrad (1) or _wgrad (2)
+// would write this output past the caches.
+int mx_internal_linear_streams(const mx_linear_desc* desc, int call, const void* out, mx_dtype dtype, int64_t ld) {
+  const mx::LinOp op = call == 1 ? mx::LIN_DGRAD : call == 2 ? mx::LIN_WGRAD : mx::LIN_FWD;
+  return check_desc(desc) == MX_OK && mx::lin_product_streams(mx::make_lin_geom(desc), op, out, dtype, ld) ? 1 : 0;
+}
+
 size_t mx_grad_workspace_bytes(int32_t count) { return count > 0 ? mx::grad_workspace_bytes(count) : 0; }
 
 mx_status mx_grad_norm(const mx_grad_list* list, float* norm, void* workspace, size_t ws_bytes, hipStream_t stream) {

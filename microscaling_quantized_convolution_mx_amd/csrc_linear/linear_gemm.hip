@@ -501,6 +501,20 @@ LinVariant lin_product_variant(const LinGeom& g, LinOp op) {
   return variant(make_plan(g, op));
 }
 
+// Whether the product writes past the caches: outputs that the last-level cache
+// cannot hold (16 experts' 4096x4096 fp32 gradients: 202 us, 258 through the
+// caches); smaller ones stay in it for the next layer (4096x4096 bf16: 46 us
+// with a quantization of the result, 48 past the caches).  Rows that do not
+// start at multiples of 64 bytes go through the caches, which join the lines
+// that two stores share (8200x16391x128 bf16: 69 us, 117 past them; 16400 columns
+// 66 and 96; 16416, whole 64 bytes, 66 and 62).
+bool lin_product_streams(const LinGeom& g, LinOp op, const void* out, mx_dtype dtype, int64_t ld) {
+  const int64_t rows = op == LIN_WGRAD ? g.n * g.ew : g.m, cols = op == LIN_FWD ? g.n : g.k;
+  const uint64_t size = dtype == MX_F32 ? 4 : 2;
+  if (static_cast<uint64_t>(rows * cols) * size < kStreamOutBytes) return false;
+  return (reinterpret_cast<uintptr_t>(out) | static_cast<uint64_t>(ld) * size) % 64 == 0;
+}
+
 size_t lin_product_workspace(const LinGeom& g, LinOp op) {
   if (g.m == 0 || (op != LIN_WGRAD && lin_few(g))) return 0;
   const Plan pl = make_plan(g, op);
@@ -538,12 +552,7 @@ hipError_t launch_lin_product(const LinGeom& g, LinOp op, const mx_linear_qtenso
   p.out = split ? workspace : out;
   p.ld = split ? pcols : ld;
   p.split_out = p.rows * pcols;
-  // outputs that the last-level cache cannot hold (16 experts' 4096x4096 fp32
-  // gradients: 218 us, 259 through the caches); smaller ones stay in it for the
-  // next layer (4096x4096 bf16: 46 us with a quantization of the result, 48 past
-  // the caches)
-  const size_t bytes = static_cast<size_t>(p.rows) * p.cols * (op == LIN_WGRAD ? g.ew : 1) * (dtype == MX_F32 ? 4 : 2);
-  p.stream = !split && bytes >= kStreamOutBytes;
+  p.stream = !split && lin_product_streams(g, op, out, dtype, ld);
   p.tokens = static_cast<int>(g.m);
   p.offsets = offsets;
   p.experts = g.e;

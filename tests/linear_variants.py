@@ -57,3 +57,12 @@ FEW_TOKENS = [
     ((999, 300, 260, [0] * 40 + [999] + [0] * 23), 2, 2, (2, True)),
     ((301, 300, 260, [301] + [0] * 39), 1, 1, (1, True)),
 ]
+
+
+def streams(d, call: int, out: int, dtype: int, ld: int) -> bool:
+    """Whether `call` would write its output, at this address and row stride, past the caches."""
+    ML._load()
+    f = mx.lib().mx_internal_linear_streams
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.POINTER(mx.mx_linear_desc), ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64]
+    return bool(f(d, call, out, dtype, ld))

@@ -101,3 +101,19 @@ def test_tokens_are_quantized_on_the_way_below_2_24_elements(m, n, k, e, fused):
     assert v.kernel == (V.FUSED if fused else V.FEW)
     groups = -(-(-(-n // 32)) // v.size)
     assert (m * -(-k // 128) * 128 * groups < 2 ** 24) == fused
+
+
+@pytest.mark.parametrize("shape,call,dtype,cols,want", [
+    ((8200, 16384, 128, 0), V.FWD, mx.MX_BF16, 16384, True), ((8200, 16384, 128, 0), V.FWD, mx.MX_BF16, 16416, True),
+    ((8200, 16384, 128, 0), V.FWD, mx.MX_BF16, 16400, False), ((8200, 16384, 128, 0), V.FWD, mx.MX_BF16, 16391, False),
+    ((8200, 8192, 128, 0), V.FWD, mx.MX_F32, 8192, True), ((8200, 8192, 128, 0), V.FWD, mx.MX_F32, 8208, True),
+    ((8200, 8192, 128, 0), V.FWD, mx.MX_F32, 8196, False), ((8200, 8192, 128, 0), V.FWD, mx.MX_F16, 8192, False),
+    ((8200, 128, 16384, 0), V.DGRAD, mx.MX_F16, 16384, True), ((8200, 128, 16384, 0), V.DGRAD, mx.MX_F16, 16385, False),
+    ((100, 4096, 4096, 16), V.WGRAD, mx.MX_F32, 4096, True), ((100, 4096, 4096, 16), V.WGRAD, mx.MX_F32, 4100, False),
+    ((100, 4096, 4096, 0), V.WGRAD, mx.MX_F32, 4096, False), ((4096, 4096, 4096, 0), V.FWD, mx.MX_BF16, 4096, False)])
+def test_outputs_past_the_caches_have_rows_of_whole_64_bytes(shape, call, dtype, cols, want):
+    """Rows that share lines are slower past the caches than through them."""
+    m, n, k, e = shape
+    d = mx.linear_desc(m, n, k, experts=e)
+    assert V.streams(d, call, 0x10000, dtype, cols) == want
+    assert not V.streams(d, call, 0x10020, dtype, cols)
