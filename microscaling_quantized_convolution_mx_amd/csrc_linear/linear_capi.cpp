@@ -259,9 +259,10 @@ mx_status mx_internal_linear_variant(const mx_linear_desc* desc, int call, int64
   return MX_OK;
 }
 
-// Not part of the ABI: whether mx_linear_fwd (0), _dgrad (1) or _wgrad (2)
-// would write this output past the caches.
+// Not part of the ABI: whether mx_linear_fwd (0), _dgrad (1), _wgrad (2) or
+// _dequantize (4, from the row form) would write this output past the caches.
 int mx_internal_linear_streams(const mx_linear_desc* desc, int call, const void* out, mx_dtype dtype, int64_t ld) {
+  if (call == 4) return mx::lin_dequantize_streams(out, dtype, ld) ? 1 : 0;
   const mx::LinOp op = call == 1 ? mx::LIN_DGRAD : call == 2 ? mx::LIN_WGRAD : mx::LIN_FWD;
   return check_desc(desc) == MX_OK && mx::lin_product_streams(mx::make_lin_geom(desc), op, out, dtype, ld) ? 1 : 0;
 }

@@ -510,9 +510,8 @@ LinVariant lin_product_variant(const LinGeom& g, LinOp op) {
 // 66 and 96; 16416, whole 64 bytes, 66 and 62).
 bool lin_product_streams(const LinGeom& g, LinOp op, const void* out, mx_dtype dtype, int64_t ld) {
   const int64_t rows = op == LIN_WGRAD ? g.n * g.ew : g.m, cols = op == LIN_FWD ? g.n : g.k;
-  const uint64_t size = dtype == MX_F32 ? 4 : 2;
-  if (static_cast<uint64_t>(rows * cols) * size < kStreamOutBytes) return false;
-  return (reinterpret_cast<uintptr_t>(out) | static_cast<uint64_t>(ld) * size) % 64 == 0;
+  const int64_t size = dtype == MX_F32 ? 4 : 2;
+  return static_cast<size_t>(rows * cols * size) >= kStreamOutBytes && whole_lines(out, ld * size);
 }
 
 size_t lin_product_workspace(const LinGeom& g, LinOp op) {

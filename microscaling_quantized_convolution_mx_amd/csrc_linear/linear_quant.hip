@@ -21,7 +21,7 @@
 // TB/s, a large copy's rate), 83 for both.  SR adds a 64-bit multiplicative hash
 // per two elements and is bound by those integer operations, 1.0e12 elements/s:
 // 131 us; neither other ways to encode nor half as many registers change that.
-// Dequantizing to bf16 takes 51 us (6.7 TB/s).
+// Dequantizing to bf16 takes 50 us (6.8 TB/s).
 #include <type_traits>
 
 #include "linear.h"
@@ -188,10 +188,13 @@ __device__ __forceinline__ void decode(uint32_t w, float scale, T* y) {
 }
 
 // Workgroups of 128 rows x 128 columns as in the quantizer; wave w takes 16
-// rows, a lane 16 bytes of them at a time, so that a store covers whole rows.  COLS: from the column form, where a lane's 16 bytes are
-// a column of 32 rows.  ALIGNED: rows start at multiples of 16 bytes; others
-// are written through the cache, which joins the lines that two stores share
-// (8192x8191 bf16: 36 us, 67 past it).
+// rows, a lane 16 bytes of them at a time, so that a store covers whole rows.
+// COLS: from the column form, where a lane's 16 bytes are a column of 32 rows
+// and a store writes one element of 64 columns (16384x8192 bf16 71 us, fp32
+// 117; from the row form 50 and 98).  ALIGNED: rows start at
+// multiples of 64 bytes; others are written through the caches, which join the
+// lines that two stores share (8192x8191 bf16: 33 us, 67 past them; 16384x8200
+// 97 and 120; 16384x8224, whole 64 bytes, 85 and 51).
 template <class T, bool COLS, bool ALIGNED>
 __global__ __launch_bounds__(512) void k_lin_dequantize(const QuantParams p, T* __restrict__ dst) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -303,9 +306,8 @@ void quantize_as(const QuantParams& p, dim3 grid, int block, bool sr, hipStream_
 }
 
 template <class T>
-void dequantize_as(const QuantParams& p, dim3 grid, mx_form form, void* dst, hipStream_t s) {
+void dequantize_as(const QuantParams& p, dim3 grid, mx_form form, void* dst, bool aligned, hipStream_t s) {
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, dim3(512), 0, s, p, static_cast<T*>(dst)); };
-  const bool aligned = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && p.ld * static_cast<int64_t>(sizeof(T)) % 16 == 0;
   if (form == MX_FORM_COLS) go(k_lin_dequantize<T, true, false>);
   else aligned ? go(k_lin_dequantize<T, false, true>) : go(k_lin_dequantize<T, false, false>);
 }
@@ -329,15 +331,18 @@ hipError_t launch_lin_quantize(const LinGeom& g, mx_role role, int block, const 
   return hipGetLastError();
 }
 
+bool lin_dequantize_streams(const void* dst, mx_dtype dtype, int64_t ld) { return whole_lines(dst, ld * (dtype == MX_F32 ? 4 : 2)); }
+
 hipError_t launch_lin_dequantize(const LinGeom& g, mx_role role, mx_form form, const mx_linear_qtensor* q, void* dst,
                                  mx_dtype dtype, int64_t ld, const int32_t* offsets, hipStream_t s) {
   QuantParams p = make_params(g, role, ld, offsets, q);
   const dim3 grid = make_grid(g, role, kPad, p);
   if (grid.x == 0) return hipSuccess;
+  const bool aligned = lin_dequantize_streams(dst, dtype, ld);
   switch (dtype) {
-    case MX_BF16: dequantize_as<bf16_t>(p, grid, form, dst, s); break;
-    case MX_F16: dequantize_as<f16_t>(p, grid, form, dst, s); break;
-    default: dequantize_as<float>(p, grid, form, dst, s); break;
+    case MX_BF16: dequantize_as<bf16_t>(p, grid, form, dst, aligned, s); break;
+    case MX_F16: dequantize_as<f16_t>(p, grid, form, dst, aligned, s); break;
+    default: dequantize_as<float>(p, grid, form, dst, aligned, s); break;
   }
   return hipGetLastError();
 }

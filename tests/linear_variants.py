@@ -9,7 +9,7 @@ from collections import namedtuple
 import microscaling_quantized_convolution_mx_amd as mx
 from microscaling_quantized_convolution_mx_amd import linear as ML
 
-FWD, DGRAD, WGRAD, APPLY = range(4)
+FWD, DGRAD, WGRAD, APPLY, DEQUANTIZE = range(5)
 NONE, FEW, FUSED, PRODUCT = range(4)
 Variant = namedtuple("Variant", "kernel size splits threads workgroups")
 

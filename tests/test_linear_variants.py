@@ -117,3 +117,12 @@ def test_outputs_past_the_caches_have_rows_of_whole_64_bytes(shape, call, dtype,
     d = mx.linear_desc(m, n, k, experts=e)
     assert V.streams(d, call, 0x10000, dtype, cols) == want
     assert not V.streams(d, call, 0x10020, dtype, cols)
+
+
+@pytest.mark.parametrize("dtype,ld,want", [
+    (mx.MX_BF16, 8192, True), (mx.MX_BF16, 8224, True), (mx.MX_BF16, 8208, False), (mx.MX_BF16, 8200, False), (mx.MX_BF16, 8191, False),
+    (mx.MX_F32, 8208, True), (mx.MX_F32, 8200, False), (mx.MX_F32, 8196, False), (mx.MX_F16, 32, True), (mx.MX_F16, 8, False)])
+def test_dequantized_rows_past_the_caches_are_of_whole_64_bytes(dtype, ld, want):
+    d = mx.linear_desc(100, 128, ld)
+    assert V.streams(d, V.DEQUANTIZE, 0x10000, dtype, ld) == want
+    assert not V.streams(d, V.DEQUANTIZE, 0x10010, dtype, ld)
