@@ -193,12 +193,11 @@ def _stream(stream, *devices) -> int | None:
     the tensors then have to share one."""
     if _current_device is None:
         _bind_torch()
-    dev = None
     if stream is None:
         dev = _current_device()
         handle = _current_stream(dev)
     elif isinstance(stream, int):
-        handle = stream
+        handle, dev = stream, None
     else:
         handle, dev = stream.cuda_stream, getattr(stream, "device_index", None)
     for at in devices:

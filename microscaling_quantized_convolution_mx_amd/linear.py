@@ -98,12 +98,10 @@ def _dims(d: mx_linear_desc, role: int):
     return d.tokens, (d.out_features if role == _mx.MX_ROLE_GRAD else d.in_features)
 
 
-def _device(t, what: str) -> int:
-    """Index of the device whose memory holds t."""
-    at = t.get_device()
-    if at < 0 and not t.is_cuda:
+def _in_host_memory(t, what: str) -> None:
+    """Refuses a tensor without a device index that is in host memory."""
+    if not t.is_cuda:
         raise ValueError(f"{what}: must be in device memory, got a {t.device.type} tensor")
-    return at
 
 
 def _matrix(t, shape, what: str):
@@ -119,7 +117,9 @@ def _matrix(t, shape, what: str):
         raise ValueError(f"{what}: must be float32, bfloat16 or float16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
-    at = _device(t, what)
+    at = t.get_device()
+    if at < 0:
+        _in_host_memory(t, what)
     if t.is_contiguous():
         return t.data_ptr() or None, dt, shape[-1], at
     st = t.stride()
@@ -144,7 +144,9 @@ def _offsets(d: mx_linear_desc, t):
         raise ValueError("offsets: must be a contiguous int32 tensor")
     if t.numel() != d.experts + 1:
         raise ValueError(f"offsets: {t.numel()} values, the call needs {d.experts + 1}")
-    at = _device(t, "offsets")
+    at = t.get_device()
+    if at < 0:
+        _in_host_memory(t, "offsets")
     return t.data_ptr(), at
 
 
@@ -154,7 +156,9 @@ def _bytes(t, what: str):
         return None, 0, None
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    at = _device(t, what)
+    at = t.get_device()
+    if at < 0:
+        _in_host_memory(t, what)
     return t.data_ptr() or None, t.numel() * t.element_size(), at
 
 
@@ -193,10 +197,11 @@ class LinearQTensor:
 
 
 def _q(q, d: mx_linear_desc, role: int, forms, what: str):
-    """The mx_linear_qtensor of q, after checking that its buffers of `forms`
-    hold what the call needs.  An mx_linear_qtensor struct passes unchecked."""
+    """(mx_linear_qtensor, device) of q, after checking that its buffers of
+    `forms` hold what the call needs.  An mx_linear_qtensor struct passes
+    unchecked."""
     if q is None or isinstance(q, mx_linear_qtensor):
-        return q
+        return q, None
     if not isinstance(q, LinearQTensor):
         raise TypeError(f"{what}: expected a LinearQTensor or an mx_linear_qtensor, got {type(q).__name__}")
     same = q.role == role and q.desc == bytes(d)  # sized for this very call
@@ -209,12 +214,7 @@ def _q(q, d: mx_linear_desc, role: int, forms, what: str):
             raise ValueError(f"{what}: {have[0]} bytes of codes, the call needs {L.mx_linear_code_bytes(d, role, form)}")
     if not q.is_cuda:
         raise ValueError(f"{what}: must be in device memory")
-    return q.c
-
-
-def _index(q):
-    """Device index of a LinearQTensor; raw addresses have none."""
-    return q.device_index if isinstance(q, LinearQTensor) else None
+    return q.c, q.device_index
 
 
 def _check(status: int, where: str) -> None:
@@ -227,18 +227,18 @@ def mx_linear_quantize(d: mx_linear_desc, role: int, src, dst, rounding: int = 0
     """Fills the forms that dst has."""
     L = _load()
     p, dt, ld, at = _matrix(src, _dims(d, role), "src")
-    q = _q(dst, d, role, dst.bytes if isinstance(dst, LinearQTensor) else (), "dst")
+    q, qat = _q(dst, d, role, dst.bytes if isinstance(dst, LinearQTensor) else (), "dst")
     off, oat = _offsets(d, offsets)
     _check(L.mx_linear_quantize(d, role, p, dt, ld, off, q, rounding, seed & (2 ** 64 - 1),
-                                _mx._stream(stream, at, _index(dst), oat)), "mx_linear_quantize")
+                                _mx._stream(stream, at, qat, oat)), "mx_linear_quantize")
 
 
 def mx_linear_dequantize(d: mx_linear_desc, role: int, q, dst, form: int = MX_FORM_ROWS, offsets=None, stream=None) -> None:
     L = _load()
     p, dt, ld, at = _matrix(dst, _dims(d, role), "dst")
+    c, qat = _q(q, d, role, (form,), "q")
     off, oat = _offsets(d, offsets)
-    _check(L.mx_linear_dequantize(d, role, form, _q(q, d, role, (form,), "q"), p, dt, ld, off,
-                                  _mx._stream(stream, at, _index(q), oat)), "mx_linear_dequantize")
+    _check(L.mx_linear_dequantize(d, role, form, c, p, dt, ld, off, _mx._stream(stream, at, qat, oat)), "mx_linear_dequantize")
 
 
 def _product(name, d, q1, role1, form1, q2, role2, form2, out, role, what, workspace, offsets, stream):
@@ -246,9 +246,9 @@ def _product(name, d, q1, role1, form1, q2, role2, form2, out, role, what, works
     p, dt, ld, at = _matrix(out, _dims(d, role), what)
     ws, n, wat = _bytes(workspace, "workspace")
     off, oat = _offsets(d, offsets)
-    a = _q(q1, d, role1, (form1,), "wq" if role1 == _mx.MX_ROLE_WEIGHT else "dyq")
-    b = _q(q2, d, role2, (form2,), "xq" if role2 == _mx.MX_ROLE_ACT else "dyq")
-    _check(getattr(L, name)(d, a, b, p, dt, ld, off, ws, n, _mx._stream(stream, at, _index(q1), _index(q2), wat, oat)), name)
+    a, aat = _q(q1, d, role1, (form1,), "wq" if role1 == _mx.MX_ROLE_WEIGHT else "dyq")
+    b, bat = _q(q2, d, role2, (form2,), "xq" if role2 == _mx.MX_ROLE_ACT else "dyq")
+    _check(getattr(L, name)(d, a, b, p, dt, ld, off, ws, n, _mx._stream(stream, at, aat, bat, wat, oat)), name)
 
 
 def mx_linear_fwd(d: mx_linear_desc, wq, xq, y, workspace=None, offsets=None, stream=None) -> None:
@@ -275,9 +275,10 @@ def mx_linear_apply(d: mx_linear_desc, wq, x, y, workspace=None, offsets=None, s
     px, dx, ldx, xat = _matrix(x, (d.tokens, d.in_features), "x")
     py, dy, ldy, yat = _matrix(y, (d.tokens, d.out_features), "y")
     ws, n, wat = _bytes(workspace, "workspace")
+    w, qat = _q(wq, d, _mx.MX_ROLE_WEIGHT, (MX_FORM_ROWS,), "wq")
     off, oat = _offsets(d, offsets)
-    _check(L.mx_linear_apply(d, _q(wq, d, _mx.MX_ROLE_WEIGHT, (MX_FORM_ROWS,), "wq"), px, dx, ldx, py, dy, ldy,
-                             off, ws, n, _mx._stream(stream, xat, yat, _index(wq), wat, oat)), "mx_linear_apply")
+    _check(L.mx_linear_apply(d, w, px, dx, ldx, py, dy, ldy, off, ws, n, _mx._stream(stream, xat, yat, qat, wat, oat)),
+           "mx_linear_apply")
 
 
 class GradList:
