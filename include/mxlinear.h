@@ -47,9 +47,9 @@
  *   nothing between calls.
  * - Matrices are row-major with a row stride `ld` in elements, at least the
  *   number of columns.  The element type is an mx_dtype.  Any alignment that
- *   the type has is taken; rows at multiples of 16 bytes are read and written
- *   fastest.  W and dW are contiguous between experts: expert e starts at
- *   e * out_features * ld.
+ *   the type has is taken; rows at multiples of 16 bytes are read fastest, at
+ *   multiples of 64 written fastest.  W and dW are contiguous between experts:
+ *   expert e starts at e * out_features * ld.
  * - Codes, scales and workspace are 16-byte aligned.  Sources and
  *   destinations must not overlap (the clip's may be the same tensors).
  * - Arguments are checked on the host before anything is enqueued; a
@@ -148,7 +148,8 @@ mx_status mx_linear_apply(const mx_linear_desc* desc, const mx_linear_qtensor* w
                           size_t ws_bytes, hipStream_t stream);
 
 /* Gradients of many tensors, contiguous each, as arrays of `count` entries
- * in HOST memory (read during the call only). */
+ * in HOST memory (read during the call only).  Their elements, counted with
+ * 8192 more for each tensor, must not pass 2^43 (MX_ERR_SHAPE). */
 typedef struct {
   int32_t count;
   const void* const* grads;

@@ -3,12 +3,15 @@
 // Two launches for up to kTensors tensors (each further kTensors add two):
 //   k_grad_sum   reads every gradient once; a workgroup sums the squares of
 //                its chunks and leaves one fp64 partial
-//   k_grad_clip  every workgroup adds all partials in the same order (a few
-//                KiB from L2), so all of them hold the same norm without a
-//                launch between, then scales its chunks
+//   k_grad_clip  every workgroup adds all partials in the same order (up to 8
+//                KiB from L2 for each kTensors tensors), so all of them hold the
+//                same norm without a launch between, then scales its chunks
 // Bound by memory: two reads and one write; 818 MB of gradients in 240 tensors
-// that start anywhere take 574 us (4.3 TB/s; the norm alone 150 us, 5.5 TB/s).  Sums are fp64: the squares of
-// any finite fp32 fit, and the adds are far below the vector units' rate.
+// that start anywhere take 574 us (4.3 TB/s; the norm alone 150 us, 5.5 TB/s).
+// The partials' reads grow with the square of the tensors' number: 24 KiB for
+// each workgroup of three launches there, 0.9 MB in 105 launches for ten thousand
+// large tensors.  Sums are fp64: the squares of any finite fp32 fit, and the
+// adds are far below the vector units' rate.
 //
 // The tensors' addresses and sizes travel in the kernel's arguments, so no
 // table has to be copied to the device.  Work is dealt in chunks over all

@@ -9,14 +9,16 @@
 // of `a` in segments with a weight matrix each (ROWS), wgrad the columns in
 // segments with an output matrix each (CONTRACT).
 //
-// Measured (bf16 outputs, fp32 for wgrad): 8192x8192x8192 234 to 270 us, 4.1 to
-// 4.7 PFLOP/s; 16384x4096x4096 forward 138, weight gradient 118; 4096^3 37.
-// The MFMA is busy 61% of a workgroup's time, at 1.9 GHz of 2.4: the same
-// loop without its copies and reads reaches 5.7 PFLOP/s at 1.7 GHz, and other
-// tilings with other waits (256x256 by 8 waves, 256x128 by two workgroups per
-// CU) come out within 3% of this one, so what bounds a large product is the
-// power that operands and MFMA draw.  A single round (4096^3) also waits 9 us
-// for its first operands and its stores.
+// Measured (bf16 outputs, fp32 for wgrad): 8192x8192x8192 238 to 278 us, 4.0 to
+// 4.6 PFLOP/s; 16384x4096x4096 forward 131 to 146, weight gradient 115 to 120;
+// 4096^3 36.  In 8192^3 the MFMA is busy 61% of the time at 1.74 GHz of 2.4, in
+// the 16384x4096x4096 forward 47% at 1.92: power sets the clock, and a part of
+// the rest (of 76 us in the latter about 36) is the start and the end of each
+// round of 256 tiles, whose first operands and stores take about 9 us without
+// MFMAs by the fit of make_plan.  Experts' products run
+// at the full clock: 16 experts of 2048x2048 with 16384 uneven tokens 61 us
+// forward, 23% busy, and 118 for the weight gradient, 12%, which waits for the
+// XCDs with the most tokens (70 with even ones; its stores take 52).
 #include "internal.h"
 #include "linear.h"
 

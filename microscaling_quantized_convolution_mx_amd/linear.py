@@ -3,7 +3,8 @@
 The functions have the names of the C entry points and marshal arguments
 only; see the header for what each computes, its layouts and its errors.
 Matrices are torch tensors in device memory, float32, bfloat16 or float16,
-with unit stride along the last dimension and any stride between rows:
+with unit stride along the last dimension and any stride between rows, all of
+a call on the device of its stream:
 
     X, dX   [tokens, in_features]
     Y, dY   [tokens, out_features]
