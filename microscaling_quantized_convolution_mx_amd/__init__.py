@@ -176,7 +176,9 @@ _current_device = _current_stream = None
 
 
 def _bind_torch() -> None:
-    """torch's current device, and the current stream's handle on a device."""
+    """torch's current device, and the current stream's handle on a device
+    (not before a call needs them: programs with raw addresses and handles
+    may have no torch)."""
     global _current_device, _current_stream
     import torch
     _current_device = torch.cuda.current_device
@@ -191,9 +193,9 @@ def _stream(stream, *devices) -> int | None:
     indexes of the tensors' devices, None for what has none (raw addresses, no
     tensor).  Of a raw handle other than 0 only its caller knows the device;
     the tensors then have to share one."""
-    if _current_device is None:
-        _bind_torch()
     if stream is None:
+        if _current_device is None:
+            _bind_torch()
         dev = _current_device()
         handle = _current_stream(dev)
     elif isinstance(stream, int):
@@ -203,6 +205,8 @@ def _stream(stream, *devices) -> int | None:
     for at in devices:
         if at is not None and at != dev:
             if dev is None:
+                if _current_device is None:
+                    _bind_torch()
                 dev = at if handle else _current_device()
             if at != dev:
                 raise ValueError(f"a tensor in the memory of device {at}, the call runs on device {dev}")
