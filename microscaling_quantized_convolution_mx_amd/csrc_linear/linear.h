@@ -137,6 +137,11 @@ __device__ __forceinline__ void store16(void* p, i32x4 v) { *static_cast<i32x4_a
 // 4.0 instead of 4.1.
 __device__ __forceinline__ void stream16(void* p, i32x4 v) { __builtin_nontemporal_store(v, static_cast<i32x4_any*>(p)); }
 
+// The scaled MFMA's results and its operands, of which E2M1 uses the first half.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
+
 // An element of a matrix of type T as fp32, and back (round to nearest even).
 struct bf16_t { uint16_t v; };
 struct f16_t { _Float16 v; };

@@ -26,11 +26,8 @@
 namespace mx {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
 constexpr int kMaxWaves = 8;
-constexpr size_t kTokenLds = size_t{48} << 10;  // for a pass' codes and scales, so that three workgroups share a CU
+constexpr size_t kTokenLds = size_t{48} << 10;  // for a pass' codes and scales: three workgroups share a CU where there are that many
 constexpr int kSumStride = 33;                  // words per token of a wave's sums: no bank conflicts
 
 struct FewParams {
@@ -51,8 +48,6 @@ struct FewParams {
   int whole;               // whether an XCD takes all stripes of a pass, else an eighth
   int part;                // groups of SN stripes that it takes
 };
-
-__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
 
 // The lane's piece of what starts at p, an address that the wave has in common.
 // (The empty asm keeps the compiler from adding the lane's part first, which

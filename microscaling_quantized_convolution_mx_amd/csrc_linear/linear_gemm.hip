@@ -29,9 +29,7 @@
 namespace mx {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 template <int I>
 struct Idx {
@@ -59,8 +57,6 @@ struct ProductParams {
   int tiles_i, tiles_j;    // output tiles (ROWS with experts: tiles_i is an upper bound over all of them)
   int splits, split_steps; // pieces of the contraction and steps of each
 };
-
-__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v.x, v.y, v.z, v.w, 0, 0, 0, 0}; }
 
 // A value that all lanes have alike.
 __device__ __forceinline__ int64_t uniform(int64_t v) {
