@@ -40,13 +40,13 @@ def listed():
         dict(name="apply8 301x2500x1999", op="apply8", m=301, n=2500, k=1999, dt="f32"),
         # long prompts
         dict(name="apply8 8192x8192x8192", op="apply8", m=8192, n=8192, k=8192, dt="bf16"),
-        # a training step of a wide layer
-        dict(name="train8 16384x4096x4096", op="train8", m=16384, n=4096, k=4096, dt="bf16"),
+        # a training step of a wide layer, the weight's gradient in the weight's type
+        dict(name="train8 16384x4096x4096", op="train8", m=16384, n=4096, k=4096, dt="bf16", dw="bf16"),
         # single tokens of 32 sequences, two experts each, 64 experts: most experts get one token or none
         dict(name="experts8 apply 64x2048x1024 e64", op="experts8", m=64, n=2048, k=1024, e=64, routing=1, train=False, dt="f16"),
-        # a training step of an expert layer, tokens spread unevenly
+        # a training step of an expert layer, tokens spread unevenly, the weights' gradients in 32 bits for their sum over steps
         dict(name="experts8 train 16384x2048x2048 e16", op="experts8", m=16384, n=2048, k=2048, e=16, routing=2, train=True,
-             dt="bf16"),
+             dt="bf16", dw="f32"),
         # single tokens of 32 sequences, two of 64 experts each
         dict(name="route serve 32x2 e64 f4096", op="route", m=32, c=2, e=64, k=4096, drop=0.0, train=False, routing=3, dt="bf16"),
         # a training step of long sequences, four of 64 experts each; some choices find their expert full
@@ -67,11 +67,12 @@ def draw(rng):
     if op == "apply8":
         return dict(op=op, m=_log(rng, 1, 8192), n=_log(rng, 65, 8192), k=_log(rng, 65, 8192), dt=dt)
     if op == "train8":
-        return dict(op=op, m=_log(rng, 1, 16384), n=_log(rng, 65, 4096), k=_log(rng, 65, 4096), dt=dt)
+        return dict(op=op, m=_log(rng, 1, 16384), n=_log(rng, 65, 4096), k=_log(rng, 65, 4096), dt=dt,
+                    dw=rng.choice(["f32", dt]))
     if op == "experts8":
         e = _log(rng, 2, 64)
         return dict(op=op, m=_log(rng, 1, 16384), n=_log(rng, 65, 2048), k=_log(rng, 65, 2048), e=e,
-                    routing=rng.randrange(1 << 30), train=rng.random() < 0.5, dt=dt)
+                    routing=rng.randrange(1 << 30), train=rng.random() < 0.5, dt=dt, dw=rng.choice(["f32", dt]))
     c, m = rng.randint(1, 8), _log(rng, 1, 16384)
     k = min(_log(rng, 33, 8192), (1 << 27) // (m * c))
     return dict(op=op, m=m, c=c, e=_log(rng, c + 1, 256), k=k, drop=rng.choice([0.0, 0.03, 0.5]), train=rng.random() < 0.5,
@@ -110,7 +111,7 @@ def work(case):
         return {"bytes": m * k * b + e * n * k * q + m * n * b, "flops": 2 * m * n * k}
     # x, w and dy in; y, dx and dw out
     all_e = case["e"] if op == "experts8" else 1
-    return {"bytes": 2 * m * (k + n) * b + all_e * n * k * (b + 4), "flops": 6 * m * n * k}
+    return {"bytes": 2 * m * (k + n) * b + all_e * n * k * (b + SIZE[case["dw"]]), "flops": 6 * m * n * k}
 
 
 # ---------------------------------------------------------------- inputs
@@ -316,11 +317,12 @@ def _plain(s):
     if op == "route":
         return _route(s)
     dt, lens = s["dt"], s["lens"]
+    dtw = DTYPES[case.get("dw", case["dt"])]
     if op == "apply8":
         return (_lines(s["x"]) @ _decode(s["wc"], s["ws"]).T).to(dt)
     if op == "train8":
         w, dy = _squares(s["w"]), s["dy"]
-        return {"y": (_lines(s["x"]) @ w.T).to(dt), "dx": (_lines(dy) @ w).to(dt), "dw": _lines(dy.T) @ _lines(s["x"].T).T}
+        return {"y": (_lines(s["x"]) @ w.T).to(dt), "dx": (_lines(dy) @ w).to(dt), "dw": (_lines(dy.T) @ _lines(s["x"].T).T).to(dtw)}
     if not case["train"]:
         return torch.cat(_each(lambda i, a: a @ _decode(s["wc"][i], s["ws"][i]).T, lens, _lines(s["x"]))).to(dt)
     w = _squares(s["w"])
@@ -328,7 +330,7 @@ def _plain(s):
     # blocks of tokens do not cross from one expert's to the next one's
     _each(lambda i, p, q: torch.mm(_lines(p.T), _lines(q.T).T, out=dw[i]), lens, s["dy"], s["x"])
     return {"y": torch.cat(_each(lambda i, a: a @ w[i].T, lens, _lines(s["x"]))).to(dt),
-            "dx": torch.cat(_each(lambda i, a: a @ w[i], lens, _lines(s["dy"]))).to(dt), "dw": dw}
+            "dx": torch.cat(_each(lambda i, a: a @ w[i], lens, _lines(s["dy"]))).to(dt), "dw": dw.to(dtw)}
 
 
 # ---------------------------------------------------------------- the framework's calls
@@ -374,7 +376,7 @@ def _own(s):
     mx.mx_linear8_fwd(d, s["wq"], s["xq"], y, s["ws"], offsets=o)
     mx.mx_linear8_quantize(s["d1"], mx.MX_ROLE_GRAD, s["dy"], s["dyq"], offsets=o)
     dx = torch.empty_like(x)
-    dw = torch.empty(s["w"].shape, device=DEV)
+    dw = torch.empty(s["w"].shape, dtype=DTYPES[case["dw"]], device=DEV)
     mx.mx_linear8_dgrad(d, s["wq"], s["dyq"], dx, s["ws"], offsets=o)
     mx.mx_linear8_wgrad(d, s["dyq"], s["xq"], dw, s["ws"], offsets=o)
     return {"y": y, "dx": dx, "dw": dw}
