@@ -348,3 +348,7 @@ from .linear import (  # noqa: E402
     linear_desc, mx_grad_clip, mx_grad_list, mx_grad_norm, mx_grad_workspace_bytes, mx_linear_apply,
     mx_linear_code_bytes, mx_linear_dequantize, mx_linear_desc, mx_linear_dgrad, mx_linear_fwd, mx_linear_qtensor,
     mx_linear_quantize, mx_linear_scale_bytes, mx_linear_wgrad, mx_linear_workspace_bytes)
+# The linear layers in 8 bits (include/mxlinear8.h).
+from .linear8 import (  # noqa: E402
+    LINEAR8_EXPORTS, Linear8QTensor, mx_linear8_apply, mx_linear8_code_bytes, mx_linear8_dequantize, mx_linear8_dgrad,
+    mx_linear8_fwd, mx_linear8_quantize, mx_linear8_scale_bytes, mx_linear8_wgrad, mx_linear8_workspace_bytes)

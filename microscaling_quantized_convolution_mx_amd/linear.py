@@ -175,17 +175,17 @@ def mx_linear_workspace_bytes(d: mx_linear_desc) -> int:
     return _load().mx_linear_workspace_bytes(d)
 
 
-class LinearQTensor:
+class _QTensor:
     """Device buffers of a quantized matrix (owned by torch), in the forms asked for."""
 
     def __init__(self, d: mx_linear_desc, role: int, device="cuda", rows: bool = True, cols: bool | None = None):
-        """cols: by default where the descriptor has that form (block 32)."""
+        """cols: by default where the descriptor has that form."""
         import torch
-        self.role, self.desc = role, bytes(d)
-        cols = d.block == 32 if cols is None else cols
+        self.role, self.desc = role, self._key(d)
+        cols = self._has_cols(d) if cols is None else cols
         self.bytes, self.buffers = {}, {}
         for form, wanted in ((MX_FORM_ROWS, rows), (MX_FORM_COLS, cols)):
-            n = (mx_linear_code_bytes(d, role, form), mx_linear_scale_bytes(d, role, form))
+            n = self._form_bytes(d, role, form)
             if wanted:
                 # 16 bytes at least, so that an empty tensor has valid pointers
                 self.bytes[form] = n
@@ -197,22 +197,37 @@ class LinearQTensor:
                                      for form in (MX_FORM_ROWS, MX_FORM_COLS) for b in self.buffers.get(form, none)))
 
 
-def _q(q, d: mx_linear_desc, role: int, forms, what: str):
+class LinearQTensor(_QTensor):
+    """A matrix in 4 bits; its column form where the descriptor has one (block 32)."""
+    _key = staticmethod(bytes)
+
+    @staticmethod
+    def _has_cols(d):
+        return d.block == 32
+
+    @staticmethod
+    def _form_bytes(d, role, form):
+        L = _load()
+        return L.mx_linear_code_bytes(d, role, form), L.mx_linear_scale_bytes(d, role, form)
+
+
+def _q(q, d: mx_linear_desc, role: int, forms, what: str, kind=LinearQTensor):
     """(mx_linear_qtensor, device) of q, after checking that its buffers of
     `forms` hold what the call needs.  An mx_linear_qtensor struct passes
     unchecked."""
     if q is None or isinstance(q, mx_linear_qtensor):
         return q, None
-    if not isinstance(q, LinearQTensor):
-        raise TypeError(f"{what}: expected a LinearQTensor or an mx_linear_qtensor, got {type(q).__name__}")
-    same = q.role == role and q.desc == bytes(d)  # sized for this very call
-    L = _lib
+    if not isinstance(q, kind):
+        raise TypeError(f"{what}: expected a {kind.__name__} or an mx_linear_qtensor, got {type(q).__name__}")
+    same = q.role == role and q.desc == kind._key(d)  # sized for this very call
     for form in forms:
         have = q.bytes.get(form)
         if have is None:
             raise ValueError(f"{what}: has no {'column' if form else 'row'} form")
-        if not same and (have[0] < L.mx_linear_code_bytes(d, role, form) or have[1] < L.mx_linear_scale_bytes(d, role, form)):
-            raise ValueError(f"{what}: {have[0]} bytes of codes, the call needs {L.mx_linear_code_bytes(d, role, form)}")
+        if not same:
+            need = kind._form_bytes(d, role, form)
+            if have[0] < need[0] or have[1] < need[1]:
+                raise ValueError(f"{what}: {have[0]} bytes of codes, the call needs {need[0]}")
     if not q.is_cuda:
         raise ValueError(f"{what}: must be in device memory")
     return q.c, q.device_index
