@@ -352,3 +352,9 @@ from .linear import (  # noqa: E402
 from .linear8 import (  # noqa: E402
     LINEAR8_EXPORTS, Linear8QTensor, mx_linear8_apply, mx_linear8_code_bytes, mx_linear8_dequantize, mx_linear8_dgrad,
     mx_linear8_fwd, mx_linear8_quantize, mx_linear8_scale_bytes, mx_linear8_wgrad, mx_linear8_workspace_bytes)
+# The norm with the residual's addition (include/mxnorm.h).
+from .norm import NORM_EXPORTS, mx_norm_bwd, mx_norm_desc, mx_norm_fwd, mx_norm_workspace_bytes, norm_desc  # noqa: E402
+# The tokens' way to their experts and back (include/mxroute.h).
+from .route import (  # noqa: E402
+    ROUTE_EXPORTS, ROUTE_MAX_CHOICES, mx_route_combine, mx_route_combine_bwd, mx_route_desc, mx_route_gather,
+    mx_route_gather_bwd, mx_route_sort, mx_route_workspace_bytes, route_desc)

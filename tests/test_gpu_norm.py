@@ -1,0 +1,292 @@
+"""The norm with the residual's addition on the GPU against a plain 64-bit
+implementation, held to the error of fp32 arithmetic (norm_ref)."""
+import numpy as np
+import pytest
+import torch
+
+import linear8_ref as R8
+import microscaling_quantized_convolution_mx_amd as mx
+import norm_ref as R
+from gpu_util import say
+from test_gpu_linear import f64, rand, same, strided
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+EPS = 1e-5
+
+
+def nans(*shape, dt="f32", pad=0):
+    return strided(torch.full(shape, float("nan"), dtype=TYPES[dt]), pad, 1 if pad else 0)
+
+
+def gap_untouched(t, pad):
+    if pad:
+        full = t.as_strided((t.shape[0], t.shape[1] + pad), (t.shape[1] + pad, 1))
+        assert bool((full[:-1, t.shape[1]:] == 7.0).all())
+
+
+def tensor8(m, k):
+    q = mx.Linear8QTensor(mx.linear_desc(m, 8, k, block=1), mx.MX_ROLE_ACT, DEV, cols=False)
+    for b in q.buffers[0]:
+        b.fill_(0xFF)
+    return q
+
+
+def check_codes(q, y, err, m, k):
+    """The row form holds y, known to a relative `err`, rounded to E4M3 by its block's scale; padding is zero."""
+    codes, scales = (b.cpu().numpy() for b in q.buffers[0])
+    mp, kp = -(-m // 128) * 128, -(-k // 128) * 128
+    r, c = np.meshgrid(np.arange(mp), np.arange(kp), indexing="ij")
+    code = codes[((r // 32) * (kp // 64) + c // 64) * 2048 + (c // 32 % 2) * 1024 + (c // 16 % 2) * 512 + (r % 32) * 16 + c % 16]
+    r, c = np.meshgrid(np.arange(mp), np.arange(kp // 128), indexing="ij")
+    scale = scales[(r // 128 * (kp // 128) + c) * 128 + r % 32 * 4 + r // 32 % 4].astype(int)
+    assert not code[m:].any() and not code[:, k:].any() and not scale[m:].any()
+    top = np.abs(np.pad(y, ((0, 0), (0, kp - k)))).reshape(m, kp // 128, 128).max(2)
+    lo = np.array([R8.exponent(v) for v in (top * (1 - err)).ravel()]).reshape(top.shape) + 127
+    hi = np.array([R8.exponent(v) for v in (top * (1 + err)).ravel()]).reshape(top.shape) + 127
+    assert np.all((scale[:m] >= lo) & (scale[:m] <= hi))
+    s = np.repeat(scale[:m] - 127, 128, 1)[:, :k]
+    a = np.abs(np.ldexp(y, -s))
+    c_lo, c_hi = (R8.code_bits(R8.round_e4m3(np.minimum(a * f, 448.0))) for f in (1 - err, 1 + err))
+    got = code[:m, :k]
+    assert np.all(((got & 127) >= c_lo) & ((got & 127) <= c_hi))
+    assert np.all((got >> 7 == np.signbit(y)) | (y == 0))
+
+
+def forward_case(m, k, dt, ydt, wdt, seed=1, pad=0, residual=True, in_place=None):
+    x, r, w = rand(seed, m, k, dt=dt), rand(seed + 1, m, k, dt=dt), rand(seed + 2, k, dt=wdt).to(DEV)
+    want = (x.float() + r.float()).to(TYPES[dt]) if residual else x
+    xg, rg = strided(x, pad), strided(r, pad)
+    total = {None: nans(m, k, dt=dt, pad=pad), "x": xg, "residual": rg}[in_place]
+    y, rstd, q = nans(m, k, dt=ydt, pad=pad), torch.full((m,), float("nan"), device=DEV), tensor8(m, k)
+    d = mx.norm_desc(m, k, EPS)
+    mx.mx_norm_fwd(d, xg, w, y, residual=rg if residual else None, total=total, yq=q, rstd=rstd)
+    torch.cuda.synchronize()
+    same(f64(total), f64(want))
+    ref, rs = R.norm(f64(want), f64(w), float(np.float32(EPS)))
+    assert np.all(np.abs(f64(rstd) - rs[:, 0]) <= rs[:, 0] * (R.rstd_error(k) + R.U))
+    err = R.y_error(k)
+    assert np.all(np.abs(f64(y) - ref) <= R.bound(ref, np.abs(ref) * err, ydt))
+    check_codes(q, ref, err, m, k)
+    for t in (total, y):
+        gap_untouched(t, pad)
+    # each output alone is the same
+    y2, t2, r2, q2 = nans(m, k, dt=ydt), nans(m, k, dt=dt), torch.full((m,), float("nan"), device=DEV), tensor8(m, k)
+    x2, res = x.to(DEV), r.to(DEV) if residual else None
+    mx.mx_norm_fwd(d, x2, w, y2, residual=res)
+    mx.mx_norm_fwd(d, x2, w, residual=res, total=t2)
+    mx.mx_norm_fwd(d, x2, w, residual=res, rstd=r2)
+    mx.mx_norm_fwd(d, x2, w, residual=res, yq=q2)
+    assert torch.equal(y2, y) and torch.equal(t2, total) and torch.equal(r2, rstd)
+    assert all(torch.equal(a, b) for a, b in zip(q.buffers[0], q2.buffers[0]))
+
+
+# one, two and four pieces of 64 and 256 threads, one and two of 1024, rows read twice; odd lengths at each border
+LENGTHS = [1, 7, 8, 127, 129, 511, 513, 1000, 1024, 1025, 2048, 2049, 4096, 4100, 8192, 8193, 16384, 16385, 33000]
+
+
+@pytest.mark.parametrize("k", LENGTHS)
+def test_forward(k):
+    say("forward", k)
+    for i, dt in enumerate(TYPES):
+        forward_case(3, k, dt, list(TYPES)[(i + 1) % 3], list(TYPES)[(i + 2) % 3])
+        forward_case(3, k, dt, dt, "f32", residual=False)
+
+
+@pytest.mark.parametrize("m,k", [(1, 4096), (127, 300), (128, 256), (129, 1500), (5000, 70), (2100, 1100), (700, 9000), (600, 17000)])
+def test_forward_many_rows(m, k):
+    """More rows than workgroups, and borders of the 8-bit form's 128 rows."""
+    say("forward", m, k)
+    forward_case(m, k, "bf16", "bf16", "bf16")
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("k", [129, 1300, 9000, 17001])
+def test_forward_strides_and_in_place(k, dt):
+    for pad in (3, 8):
+        forward_case(5, k, dt, dt, "f32", pad=pad)
+    forward_case(5, k, dt, dt, "f32", in_place="x")
+    forward_case(5, k, dt, dt, "f32", pad=5, in_place="residual")
+
+
+def backward_case(m, k, dt, dydt, wdt, seed=1, pad=0, dtotal=True, in_place=None):
+    total, dy, dt_ = rand(seed, m, k, dt=dt), rand(seed + 1, m, k, dt=dydt), rand(seed + 2, m, k, dt=dt)
+    w = rand(seed + 3, k, dt=wdt).to(DEV)
+    d = mx.norm_desc(m, k, EPS)
+    rstd = torch.full((m,), float("nan"), device=DEV)
+    tg, dyg, dtg = strided(total, pad), strided(dy, pad), strided(dt_, pad)
+    mx.mx_norm_fwd(d, tg, w, rstd=rstd)
+    dx = {None: nans(m, k, dt=dt, pad=pad), "dy": dyg, "dtotal": dtg}[in_place]
+    dw = torch.full((k,), float("nan"), device=DEV)
+    ws = torch.full((mx.mx_norm_workspace_bytes(d),), 0xFF, dtype=torch.uint8, device=DEV)
+    ref, err, dwr, dwe = R.grads(f64(dy), f64(total), f64(w), f64(rstd)[:, None], f64(dt_) if dtotal else 0.0)
+    mx.mx_norm_bwd(d, dyg, tg, w, rstd, dx, dw, dtotal=dtg if dtotal else None, workspace=ws)
+    torch.cuda.synchronize()
+    assert np.all(np.abs(f64(dx) - ref) <= R.bound(ref, err, dt))
+    assert np.all(np.abs(f64(dw) - dwr) <= dwe + R.TINY["f32"])
+    gap_untouched(dx, pad)
+    if in_place is None:
+        dx2, dw2 = nans(m, k, dt=dt), torch.full((k,), float("nan"), device=DEV)
+        mx.mx_norm_bwd(d, dyg, tg, w, rstd, dx2, dtotal=dtg if dtotal else None)
+        mx.mx_norm_bwd(d, dyg, tg, w, rstd, dweight=dw2, workspace=ws)
+        assert torch.equal(dx2, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("k", LENGTHS)
+def test_backward(k):
+    say("backward", k)
+    for i, dt in enumerate(TYPES):
+        backward_case(5, k, dt, list(TYPES)[(i + 1) % 3], list(TYPES)[(i + 2) % 3])
+        backward_case(3, k, dt, dt, "f32", dtotal=False)
+
+
+@pytest.mark.parametrize("m,k", [(1, 4096), (127, 300), (5000, 70), (2100, 1100), (700, 9000), (600, 17000)])
+def test_backward_many_rows(m, k):
+    say("backward", m, k)
+    backward_case(m, k, "bf16", "bf16", "bf16")
+    backward_case(m, k, "f32", "f32", "f32")
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("k", [129, 1300, 9000, 17001])
+def test_backward_strides_and_in_place(k, dt):
+    for pad in (3, 8):
+        backward_case(5, k, dt, dt, "f32", pad=pad)
+    backward_case(5, k, dt, dt, "f32", in_place="dy")
+    backward_case(5, k, dt, dt, "f32", pad=5, in_place="dtotal")
+
+
+def test_gradients_are_differences():
+    """Central differences of the 64-bit <dy, y> + <dtotal, total> against the
+    GPU's gradients.  Row lengths are near 1, where the loss' third derivative
+    is at most some tens of its terms: with a step of 2^-13 the quotient is off
+    by less than 2^-26 * 10 of them, and by 2^-52 / 2^-13 of the loss."""
+    m, k = 4, 37
+    g = np.random.default_rng(3)
+    x, w, dy, dt = (g.standard_normal(s) for s in ((m, k), (k,), (m, k), (m, k)))
+    x, w, dy, dt = (a.astype(np.float32).astype(np.float64) for a in (x, w, dy, dt))
+    d = mx.norm_desc(m, k, EPS)
+    t = lambda a: torch.from_numpy(a.astype(np.float32)).to(DEV)  # noqa: E731
+    rstd, dx, dw = torch.empty(m, device=DEV), torch.empty(m, k, device=DEV), torch.empty(k, device=DEV)
+    mx.mx_norm_fwd(d, t(x), t(w), rstd=rstd)
+    ws = torch.empty(mx.mx_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+    mx.mx_norm_bwd(d, t(dy), t(x), t(w), rstd, dx, dw, dtotal=t(dt), workspace=ws)
+
+    def loss(x, w):
+        return float((dy * R.norm(x, w, float(np.float32(EPS)))[0]).sum() + (dt * x).sum())
+    _, err, _, dwe = R.grads(dy, x, w, f64(rstd)[:, None], dt)
+    terms = np.abs(dy).sum() * np.abs(w).max() + np.abs(dt * x).sum()
+    slack = terms * (10 * 2.0 ** -26 + 2.0 ** -38)
+    # (the GPU's rstd is off by its own rounding, which the gradient takes up to three times)
+    more = 3 * R.rstd_error(k)
+    h = 2.0 ** -13
+    for i, j in ((0, 0), (1, 36), (3, 17), (2, 5)):
+        a, b = x.copy(), x.copy()
+        a[i, j] += h
+        b[i, j] -= h
+        q = (loss(a, w) - loss(b, w)) / (2 * h)
+        got = f64(dx)[i, j]
+        assert abs(got - q) <= slack + R.bound(got, err[i, j], "f32") + more * (np.abs(dy[i] * w).max() * 3 + abs(dt[i, j]))
+    for j in (0, 20, 36):
+        a, b = w.copy(), w.copy()
+        a[j] += h
+        b[j] -= h
+        q = (loss(x, a) - loss(x, b)) / (2 * h)
+        assert abs(f64(dw)[j] - q) <= slack + dwe[j] + more * np.abs(dy[:, j]).sum() * 3
+
+
+def test_special_values():
+    """A row with a NaN or an Inf is its own; rows of zeros stay zeros, unless eps is 0."""
+    m, k = 6, 300
+    x = rand(1, m, k)
+    x[1, 7], x[2, 290], x[3] = float("nan"), float("inf"), 0.0
+    w = torch.ones(k, device=DEV)
+    y, q = nans(m, k), tensor8(m, k)
+    mx.mx_norm_fwd(mx.norm_desc(m, k, EPS), x.to(DEV), w, y, yq=q)
+    ny = np.isnan(f64(y))
+    assert ny[1].all() and ny[2, 290] and not ny[2, :290].any() and not ny[[0, 3, 4, 5]].any()
+    assert not f64(y)[3].any() and not f64(y)[2, :290].any()
+    v = torch.empty(m, k, device=DEV)
+    mx.mx_linear8_dequantize(mx.linear_desc(m, 8, k, block=1), mx.MX_ROLE_ACT, q, v)
+    nv = np.isnan(f64(v))
+    assert nv[1].all() and nv[2, 256:].all() and not nv[2, :256].any() and not nv[[0, 3, 4, 5]].any()
+    assert not f64(v)[3].any()
+    mx.mx_norm_fwd(mx.norm_desc(m, k, 0.0), x.to(DEV), w, y)
+    assert np.isnan(f64(y)[3]).all() and not np.isnan(f64(y)[[0, 4, 5]]).any()
+
+
+def test_no_tokens():
+    k = 300
+    d = mx.norm_desc(0, k)
+    x, w, dw = torch.empty(0, k, device=DEV), torch.ones(k, device=DEV), torch.full((k,), 5.0, device=DEV)
+    assert mx.mx_norm_workspace_bytes(d) == 0
+    mx.mx_norm_fwd(d, x, w, torch.empty_like(x), total=torch.empty_like(x), yq=tensor8(0, k), rstd=torch.empty(0, device=DEV))
+    mx.mx_norm_fwd(d, x, w, torch.empty_like(x))
+    mx.mx_norm_bwd(d, x, x, w, torch.empty(0, device=DEV), torch.empty_like(x), dw)
+    mx.mx_norm_bwd(d, x, x, w, torch.empty(0, device=DEV), torch.empty_like(x))
+    torch.cuda.synchronize()
+    assert not bool(dw.any())
+
+
+def test_graph_stream_and_repeatability():
+    m, k = 300, 2500
+    d = mx.norm_desc(m, k)
+    x, r, w, dy, dt = (t.to(DEV) for t in (rand(1, m, k), rand(2, m, k), rand(3, k), rand(4, m, k), rand(5, m, k)))
+    out = [torch.empty_like(x), torch.empty_like(x), torch.empty(m, device=DEV), torch.empty_like(x), torch.empty(k, device=DEV)]
+    q = tensor8(m, k)
+    ws = torch.empty(mx.mx_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+
+    def step():
+        mx.mx_norm_fwd(d, x, w, out[0], residual=r, total=out[1], yq=q, rstd=out[2])
+        mx.mx_norm_bwd(d, dy, out[1], w, out[2], out[3], out[4], dtotal=dt, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        x.copy_(rand(20 + i, m, k))
+        dy.copy_(rand(30 + i, m, k))
+        for t in (*out, ws, *q.buffers[0]):
+            t.view(torch.uint8).fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (*out, *q.buffers[0])]
+        for t in (*out, ws, *q.buffers[0]):
+            t.view(torch.uint8).fill_(0xFF)
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, (*out, *q.buffers[0])):
+            assert torch.equal(a, b)
+
+
+def test_matrices_past_32_bits():
+    """More than 2^32 elements: the last rows."""
+    m, k = 40000, 110016
+    d = mx.norm_desc(m, k, EPS)
+    x = torch.empty(m, k, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, m, 8000):
+        x[a:a + 8000] = torch.randn(min(8000, m - a), k, device=DEV, dtype=torch.bfloat16)
+    tail = x[m - 3:].cpu()
+    w = torch.ones(k, device=DEV)
+    rstd, y = torch.empty(m, device=DEV), torch.empty_like(x)
+    mx.mx_norm_fwd(d, x, w, y, rstd=rstd)
+    ref, _ = R.norm(f64(tail), np.ones(k), float(np.float32(EPS)))
+    assert np.all(np.abs(f64(y[m - 3:]) - ref) <= R.bound(ref, np.abs(ref) * R.y_error(k), "bf16"))
+    dw = torch.empty(k, device=DEV)
+    ws = torch.empty(mx.mx_norm_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+    mx.mx_norm_bwd(d, x, x, w, rstd, y, dw, workspace=ws)
+    dx, err, _, _ = R.grads(f64(tail), f64(tail), np.ones(k), f64(rstd[m - 3:])[:, None], 0.0)
+    assert np.all(np.abs(f64(y[m - 3:]) - dx) <= R.bound(dx, err, "bf16"))
+    # every row's <dy, h> adds to the gradient: columns at random, in 64 bits
+    at = torch.tensor([0, 77777, k - 1], device=DEV)
+    c = x[:, at].double()
+    h = c * rstd.double()[:, None]
+    ref, lim = f64((c * h).sum(0)), (m + 3) * R.U * 1.01 * f64((c * h).abs().sum(0))
+    assert np.all(np.abs(f64(dw[at]) - ref) <= lim)

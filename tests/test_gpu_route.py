@@ -1,0 +1,295 @@
+"""The tokens' way to their experts and back on the GPU against a plain
+implementation: places must agree exactly, sums are held to the error of fp32
+sums of as many terms, rounded once."""
+import numpy as np
+import pytest
+import torch
+
+import microscaling_quantized_convolution_mx_amd as mx
+from gpu_util import say
+from norm_ref import TINY, U, bound
+from test_gpu_linear import f64, rand, same, strided
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def choices(seed, m, c, e, drop=0.0, skew=0.0):
+    """Experts of each token; some choices outside the range."""
+    g = np.random.default_rng(seed)
+    p = np.exp(skew * g.standard_normal(e))
+    a = g.choice(e, size=(m, c), p=p / p.sum()).astype(np.int32)
+    bad = g.choice(np.array([-1, -7, e, 2 ** 31 - 1, -2 ** 31], np.int64), size=(m, c)).astype(np.int32)
+    return np.where(g.random((m, c)) < drop, bad, a).astype(np.int32)
+
+
+def places(expert, e):
+    """offsets, rows and order, choice by choice."""
+    flat = expert.ravel()
+    valid = (flat >= 0) & (flat < e)
+    order = np.flatnonzero(valid)
+    order = order[np.argsort(flat[order], kind="stable")]
+    rows = np.full(flat.size, -1, np.int32)
+    rows[order] = np.arange(order.size)
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat[valid], minlength=e))]).astype(np.int32)
+    full = np.full(flat.size, -1, np.int32)
+    full[:order.size] = order
+    return offsets, rows.reshape(expert.shape), full
+
+
+def sort(expert, e, order=True, fill=0xFF):
+    m, c = expert.shape
+    d = mx.route_desc(m, c, e, 1)
+    t = [torch.full((n,), 77, dtype=torch.int32, device=DEV) for n in (e + 1, m * c, m * c)]
+    ws = torch.full((max(16, mx.mx_route_workspace_bytes(d)),), fill, dtype=torch.uint8, device=DEV)
+    mx.mx_route_sort(d, torch.from_numpy(expert).to(DEV), t[0], t[1].view(m, c), t[2] if order else None, ws)
+    torch.cuda.synchronize()
+    return [v.cpu().numpy() for v in t]
+
+
+@pytest.mark.parametrize("m,c,e", [
+    (1, 1, 1), (1, 2, 64), (5, 3, 7), (32, 2, 64), (63, 1, 2), (64, 1, 3), (65, 1, 5), (1000, 4, 64), (1023, 4, 1024), (1024, 4, 128),
+    (1025, 4, 65), (4097, 1, 1), (5000, 8, 256), (9999, 6, 1000), (16384, 4, 64), (40000, 8, 160), (70000, 64, 33)])
+@pytest.mark.parametrize("drop,skew", [(0.0, 0.0), (0.3, 2.0)])
+def test_sort(m, c, e, drop, skew):
+    say("sort", m, c, e, drop)
+    expert = choices(m + c, m, c, e, drop, skew)
+    offsets, rows, order = places(expert, e)
+    got = sort(expert, e)
+    same(got[0], offsets)
+    same(got[1].reshape(m, c), rows)
+    same(got[2], order)
+    got = sort(expert, e, order=False, fill=0)
+    same(got[0], offsets)
+    same(got[1].reshape(m, c), rows)
+    assert (got[2] == 77).all()
+
+
+@pytest.mark.parametrize("m", [100, 6000])
+@pytest.mark.parametrize("what", ["one expert", "all dropped", "the last expert"])
+def test_sort_extremes(m, what):
+    e = 9
+    expert = np.full((m, 2), {"one expert": 4, "all dropped": -1, "the last expert": e - 1}[what], np.int32)
+    offsets, rows, order = places(expert, e)
+    got = sort(expert, e)
+    same(got[0], offsets)
+    same(got[1].reshape(m, 2), rows)
+    same(got[2], order)
+
+
+def test_sort_of_no_tokens():
+    d = mx.route_desc(0, 2, 5, 64)
+    offsets = torch.full((6,), 9, dtype=torch.int32, device=DEV)
+    none, x = torch.empty(0, 2, dtype=torch.int32, device=DEV), torch.empty(0, 64, device=DEV)
+    assert mx.mx_route_workspace_bytes(d) == 0
+    mx.mx_route_sort(d, none, offsets, none, none.view(0))
+    w = torch.empty(0, 2, device=DEV)
+    mx.mx_route_gather(d, x, none, x)
+    mx.mx_route_gather_bwd(d, x, none, x)
+    mx.mx_route_combine(d, x, none, w, x)
+    mx.mx_route_combine_bwd(d, x, x, none, w, x, w)
+    torch.cuda.synchronize()
+    assert not bool(offsets.any())
+
+
+def nans(*shape, dt="f32", pad=0):
+    return strided(torch.full(shape, float("nan"), dtype=TYPES[dt]), pad, 1 if pad else 0)
+
+
+def gap_untouched(t, pad):
+    if pad:
+        full = t.as_strided((t.shape[0], t.shape[1] + pad), (t.shape[1] + pad, 1))
+        assert bool((full[:-1, t.shape[1]:] == 7.0).all())
+
+
+def move_case(m, c, e, k, dt, drop=0.2, pad=0, seed=1, rows=None):
+    """All four moves on rows of a sort (or given ones)."""
+    g = np.random.default_rng(seed)
+    if rows is None:
+        rows = places(choices(seed, m, c, e, drop), e)[1]
+    rt = torch.from_numpy(rows).to(DEV)
+    kept = (rows >= 0) & (rows < m * c)
+    used = np.zeros(m * c, bool)
+    used[rows[kept]] = True
+    d = mx.route_desc(m, c, e, k)
+    x, y, dout = (rand(seed + i, n, k, dt=dt) for i, n in ((1, m), (2, m * c), (3, m)))
+    weight = torch.from_numpy(g.standard_normal((m, c)).astype(np.float32)).to(DEV)
+    xg, yg, dg = (strided(t, pad) for t in (x, y, dout))
+    xv, yv, dv, wv = f64(x), f64(y), f64(dout), f64(weight)
+    at = np.where(kept, rows, 0)
+
+    # gather: copies, and nothing in the rows of no choice
+    out = nans(m * c, k, dt=dt, pad=pad)
+    mx.mx_route_gather(d, xg, rt, out)
+    want = np.full((m * c, k), np.nan)
+    for j in range(c):
+        want[rows[kept[:, j], j]] = xv[kept[:, j]]
+    same(f64(out), want)
+    gap_untouched(out, pad)
+
+    # combine and gather_bwd; one product and one sum per choice
+    for w, name in ((wv, "combine"), (np.ones((m, c)), "gather_bwd")):
+        out = nans(m, k, dt=dt, pad=pad)
+        mx.mx_route_combine(d, yg, rt, weight, out) if name == "combine" else mx.mx_route_gather_bwd(d, yg, rt, out)
+        ref, mags = np.zeros((m, k)), np.zeros((m, k))
+        for j in range(c):
+            v = np.where(kept[:, j, None], yv[at[:, j]], 0.0) * w[:, j, None]
+            ref += v
+            mags += np.abs(v)
+        assert np.all(np.abs(f64(out) - ref) <= bound(ref, (c + 1) * U * 1.01 * mags + c * 2.0 ** -149, dt)), name
+        gap_untouched(out, pad)
+
+    # combine_bwd
+    dy, dw = nans(m * c, k, dt=dt, pad=pad), torch.full((m, c), float("nan"), device=DEV)
+    mx.mx_route_combine_bwd(d, dg, yg, rt, weight, dy, dw)
+    got = f64(dy)
+    for j in range(c):
+        ref = dv * wv[:, j, None]
+        err = np.abs(got[at[:, j]] - ref)[kept[:, j]]
+        assert np.all(err <= bound(ref, U * np.abs(ref) + 2.0 ** -149, dt)[kept[:, j]])
+        terms = dv * yv[at[:, j]] * kept[:, j, None]
+        assert np.all(np.abs(f64(dw)[:, j] - terms.sum(1)) <= (k + 1) * U * 1.01 * np.abs(terms).sum(1) + k * 2.0 ** -149 + TINY["f32"])
+    assert np.isnan(got[~used]).all() and not f64(dw)[~kept].any()
+    gap_untouched(dy, pad)
+    # each of the two alone is the same
+    dy2, dw2 = nans(m * c, k, dt=dt), torch.full((m, c), float("nan"), device=DEV)
+    mx.mx_route_combine_bwd(d, dg, yg, rt, weight, dy2)
+    mx.mx_route_combine_bwd(d, dg, yg, rt, weight, dweight=dw2)
+    same(f64(dy2), got)
+    assert torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("m,c,e,k", [
+    (1, 1, 1, 1), (1, 2, 4, 4096), (3, 1, 2, 7), (32, 2, 64, 33), (33, 3, 5, 100), (100, 8, 16, 515), (65, 9, 12, 2048),
+    (20, 17, 40, 1000), (4, 64, 100, 250), (700, 4, 64, 64), (7, 2, 3, 20000)])
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_moves(m, c, e, k, dt):
+    say("moves", m, c, e, k, dt)
+    move_case(m, c, e, k, dt)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("pad", [3, 8])
+def test_moves_strided(dt, pad):
+    move_case(40, 3, 8, 129, dt, pad=pad)
+    move_case(9, 2, 8, 3000, dt, pad=pad)
+
+
+def test_moves_of_dropped_tokens():
+    """No choice kept: zeros come back, nothing is written to rows."""
+    move_case(50, 2, 4, 300, "bf16", rows=np.full((50, 2), -1, np.int32))
+
+
+def test_rows_out_of_range_count_as_dropped():
+    m, c = 30, 2
+    rows = places(choices(3, m, c, 4), 4)[1]
+    rows[::3, 0] = [m * c, 2 ** 31 - 1, -2 ** 31, -5, m * c + 1] * 2
+    move_case(m, c, 4, 200, "f32", rows=rows)
+
+
+def test_gradients_are_differences():
+    """combine is linear in y and in the weights, and gather in x: with small
+    integers all sums are exact and difference quotients equal the gradients."""
+    m, c, e, k = 12, 3, 5, 40
+    g = np.random.default_rng(2)
+    rows = places(choices(4, m, c, e, 0.2), e)[1]
+    d = mx.route_desc(m, c, e, k)
+    t = lambda a: torch.from_numpy(a.astype(np.float32)).to(DEV)  # noqa: E731
+    rt = torch.from_numpy(rows).to(DEV)
+    x, y, w, dout, drows = (g.integers(-3, 4, s).astype(float) for s in ((m, k), (m * c, k), (m, c), (m, k), (m * c, k)))
+
+    def loss(y, w):
+        out = torch.empty(m, k, device=DEV)
+        mx.mx_route_combine(d, t(y), rt, t(w), out)
+        return float((f64(out) * dout).sum())
+
+    def gathered(x):
+        out = torch.zeros(m * c, k, device=DEV)
+        mx.mx_route_gather(d, t(x), rt, out)
+        return float((f64(out) * drows).sum())
+    dy, dw, dx = torch.zeros(m * c, k, device=DEV), torch.empty(m, c, device=DEV), torch.empty(m, k, device=DEV)
+    mx.mx_route_combine_bwd(d, t(dout), t(y), rt, t(w), dy, dw)
+    mx.mx_route_gather_bwd(d, t(drows), rt, dx)
+    at, ax = loss(y, w), gathered(x)
+    for i, j in ((0, 0), (7, 39), (20, 5), (35, 11)):
+        y2 = y.copy()
+        y2[i, j] += 1
+        assert loss(y2, w) - at == f64(dy)[i, j]
+    for i, j in ((0, 0), (5, 2), (11, 1)):
+        w2 = w.copy()
+        w2[i, j] += 1
+        assert loss(y, w2) - at == f64(dw)[i, j]
+    for i, j in ((0, 0), (5, 22), (11, 39)):
+        x2 = x.copy()
+        x2[i, j] += 1
+        assert gathered(x2) - ax == f64(dx)[i, j]
+
+
+def test_graph_stream_and_repeatability():
+    m, c, e, k = 3000, 4, 32, 500
+    d = mx.route_desc(m, c, e, k)
+    x, y, dout = (rand(i, n, k, dt="bf16").to(DEV) for i, n in ((1, m), (2, m * c), (3, m)))
+    w = rand(4, m, c).to(DEV)
+    expert = torch.from_numpy(choices(1, m, c, e, 0.1)).to(DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out = [torch.empty(e + 1, **i32), torch.empty(m, c, **i32), torch.empty(m * c, **i32), torch.empty_like(y), torch.empty_like(x),
+           torch.empty_like(y), torch.empty_like(w), torch.empty_like(x)]
+    ws = torch.empty(mx.mx_route_workspace_bytes(d), dtype=torch.uint8, device=DEV)
+
+    def step():
+        mx.mx_route_sort(d, expert, out[0], out[1], out[2], ws)
+        mx.mx_route_gather(d, x, out[1], out[3])
+        mx.mx_route_combine(d, y, out[1], w, out[4])
+        mx.mx_route_combine_bwd(d, dout, y, out[1], w, out[5], out[6])
+        mx.mx_route_gather_bwd(d, out[5], out[1], out[7])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        expert.copy_(torch.from_numpy(choices(20 + i, m, c, e, 0.1)))
+        x.copy_(rand(30 + i, m, k, dt="bf16"))
+        for t in (*out, ws):
+            t.view(torch.uint8).zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for t in (*out, ws):
+            t.view(torch.uint8).zero_()
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, out):
+            assert torch.equal(a, b)
+
+
+def test_matrices_past_32_bits():
+    """Rows of more than 2^32 elements: the last tokens'."""
+    m, c, k = 60000, 2, 40000
+    d = mx.route_desc(m, c, 4, k)
+    rows = torch.arange(m * c, dtype=torch.int32, device=DEV).flip(0).view(m, c).contiguous()  # token 0 is in the last rows
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device=DEV)
+    x[:2] = rand(1, 2, k, dt="bf16").to(DEV)
+    x[-1] = rand(2, k, dt="bf16").to(DEV)
+    y = torch.empty(m * c, k, dtype=torch.bfloat16, device=DEV)
+    mx.mx_route_gather(d, x, rows, y)
+    for t, r in ((0, m * c - 1), (0, m * c - 2), (1, m * c - 3), (m - 1, 0), (m - 1, 1)):
+        assert torch.equal(y[r], x[t])
+    w = torch.full((m, c), 0.5, device=DEV)
+    out, dw = torch.empty_like(x), torch.empty(m, c, device=DEV)
+    mx.mx_route_combine(d, y, rows, w, out)
+    assert torch.equal(out, x)
+    mx.mx_route_combine_bwd(d, x, y, rows, w, dweight=dw)
+    for t in (0, 1, m - 1):
+        ref = float((f64(x[t]) ** 2).sum())
+        assert np.all(np.abs(f64(dw[t]) - ref) <= (k + 1) * U * 1.01 * ref)
+    dy = torch.empty_like(y)
+    mx.mx_route_combine_bwd(d, x, y, rows, w, dy)
+    for t, r in ((0, m * c - 1), (1, m * c - 3), (m - 1, 0)):
+        assert torch.equal(dy[r], x[t] * 0.5)

@@ -1,0 +1,247 @@
+"""C ABI and binding of the norm and the routing, without a GPU: exports, every
+refusal on the host, and tensors on the wrong device."""
+import os
+import re
+
+import pytest
+import torch
+
+import microscaling_quantized_convolution_mx_amd as mx
+from microscaling_quantized_convolution_mx_amd import norm as MN
+from microscaling_quantized_convolution_mx_amd import route as MR
+from test_linear_capi import A16, ROOT, qt
+from test_linear_devices import Stream, on
+
+
+@pytest.mark.parametrize("header,exports", [("mxnorm.h", mx.NORM_EXPORTS), ("mxroute.h", mx.ROUTE_EXPORTS)])
+def test_exports_every_declared_function(header, exports):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", header)).read(), flags=re.S)
+    names = set(re.findall(r"\b(mx_[a-z0-9_]+)\s*\(", text))
+    assert names == set(exports)
+    for n in names:
+        assert hasattr(mx.lib(), n) and hasattr(mx, n)
+
+
+# ---------------------------------------------------------------- norm
+
+ND = dict(tokens=10, features=100, eps=1e-6)
+
+
+def fwd(d="ok", x=A16, ldx=100, r=A16, ldr=100, dt=1, w=A16, wdt=0, total=A16 + 64, ldt=100, y=A16, ydt=1, ldy=100, q=None, rstd=None):
+    MN._load()
+    return mx.lib().mx_norm_fwd(mx.norm_desc(**ND) if d == "ok" else d, x, ldx, r, ldr, dt, w, wdt, total, ldt, y, ydt, ldy, q, rstd, None)
+
+
+def bwd(d="ok", dy=A16, dydt=1, lddy=100, total=A16, ldt=100, dtotal=A16, lddt=100, dt=1, w=A16, wdt=0, rstd=A16, dx=A16 + 64,
+        lddx=100, dw=A16, ws=A16, n=1 << 30):
+    MN._load()
+    return mx.lib().mx_norm_bwd(mx.norm_desc(**ND) if d == "ok" else d, dy, dydt, lddy, total, ldt, dtotal, lddt, dt, w, wdt, rstd,
+                                dx, lddx, dw, ws, n, None)
+
+
+@pytest.mark.parametrize("change", [dict(tokens=-1), dict(features=0), dict(features=-4), dict(eps=-1e-6), dict(eps=float("nan")),
+                                    dict(eps=float("inf")), dict(tokens=2 ** 31 - 1), dict(features=2 ** 31 - 1),
+                                    dict(tokens=2 ** 30, features=2 ** 30)])
+def test_norm_descriptor(change):
+    d = mx.norm_desc(**dict(ND, **change))
+    assert fwd(d) == -2 and bwd(d) == -2 and mx.mx_norm_workspace_bytes(d) == 0
+
+
+def test_norm_forward_refusals():
+    assert fwd(None) == -1 and fwd(x=None) == -1 and fwd(w=None) == -1
+    assert fwd(total=None, y=None) == -1
+    assert fwd(dt=3) == -3 and fwd(wdt=9) == -3 and fwd(ydt=-1) == -3
+    assert fwd(ldx=99) == -2 and fwd(ldr=99) == -2 and fwd(ldt=99) == -2 and fwd(ldy=99) == -2
+    assert fwd(x=A16 + 1) == -5 and fwd(r=A16 + 1) == -5 and fwd(w=A16 + 2) == -5 and fwd(total=A16 + 1) == -5
+    assert fwd(y=A16 + 1) == -5 and fwd(rstd=A16 + 2) == -5
+    assert fwd(q=qt(rows=None)) == -1 and fwd(q=qt(rs=None)) == -1 and fwd(q=qt(rows=A16 + 8)) == -5
+    # total in x's or the residual's place with other strides than theirs
+    assert fwd(total=A16, ldx=104, ldr=100, ldt=100) == -2 and fwd(total=A16, ldx=100, ldr=104, r=A16, ldt=100) == -2
+    # nothing to do: no tokens
+    assert fwd(mx.norm_desc(0, 100), x=None, r=None, total=None, y=None) == 0
+
+
+def test_norm_backward_refusals():
+    assert bwd(None) == -1 and bwd(dy=None) == -1 and bwd(total=None) == -1 and bwd(w=None) == -1 and bwd(rstd=None) == -1
+    assert bwd(dx=None, dw=None) == -1
+    assert bwd(dt=3) == -3 and bwd(dydt=9) == -3 and bwd(wdt=5) == -3
+    assert bwd(lddy=99) == -2 and bwd(ldt=99) == -2 and bwd(lddt=99) == -2 and bwd(lddx=99) == -2
+    assert bwd(dy=A16 + 1) == -5 and bwd(total=A16 + 1) == -5 and bwd(dtotal=A16 + 1) == -5 and bwd(dx=A16 + 1) == -5
+    assert bwd(rstd=A16 + 2) == -5 and bwd(dw=A16 + 2) == -5 and bwd(ws=A16 + 8) == -5
+    assert bwd(ws=None) == -6 and bwd(n=mx.mx_norm_workspace_bytes(mx.norm_desc(**ND)) - 1) == -6
+    # dx in dy's or dtotal's place with another type or other strides
+    assert bwd(dx=A16, dydt=2) == -2 and bwd(dx=A16, lddy=104) == -2 and bwd(dx=A16, lddt=104) == -2
+
+
+# ---------------------------------------------------------------- routing
+
+RD = dict(tokens=10, choices=2, experts=4, features=100)
+
+
+def rd(**change):
+    return mx.route_desc(**dict(RD, **change))
+
+
+def sort(d="ok", expert=A16, offsets=A16, rows=A16, order=A16, ws=A16, n=1 << 30):
+    MR._load()
+    return mx.lib().mx_route_sort(rd() if d == "ok" else d, expert, offsets, rows, order, ws, n, None)
+
+
+def move(name, d="ok", a=A16, lda=100, rows=A16, b=A16, ldb=100, dt=1):
+    MR._load()
+    return getattr(mx.lib(), name)(rd() if d == "ok" else d, a, lda, rows, b, ldb, dt, None)
+
+
+def combine(d="ok", y=A16, ldy=100, rows=A16, w=A16, out=A16, ldo=100, dt=1):
+    MR._load()
+    return mx.lib().mx_route_combine(rd() if d == "ok" else d, y, ldy, rows, w, out, ldo, dt, None)
+
+
+def combine_bwd(d="ok", dout=A16, ldo=100, y=A16, ldy=100, rows=A16, w=A16, dy=A16, lddy=100, dw=A16, dt=1):
+    MR._load()
+    return mx.lib().mx_route_combine_bwd(rd() if d == "ok" else d, dout, ldo, y, ldy, rows, w, dy, lddy, dw, dt, None)
+
+
+@pytest.mark.parametrize("change", [dict(tokens=-1), dict(choices=0), dict(choices=65), dict(experts=0), dict(experts=1025),
+                                    dict(tokens=2 ** 29), dict(tokens=2 ** 31 - 1, choices=64)])
+def test_route_descriptor(change):
+    d = rd(**change)
+    assert sort(d) == -2 and combine(d) == -2 and combine_bwd(d) == -2 and mx.mx_route_workspace_bytes(d) == 0
+    assert move("mx_route_gather", d) == -2 and move("mx_route_gather_bwd", d) == -2
+
+
+def test_route_refusals():
+    assert sort(None) == -1 and sort(expert=None) == -1 and sort(offsets=None) == -1 and sort(rows=None) == -1
+    for arg in ("expert", "offsets", "rows", "order"):
+        assert sort(**{arg: A16 + 2}) == -5
+    many = rd(tokens=100000)
+    assert sort(many, ws=None) == -6 and sort(many, n=mx.mx_route_workspace_bytes(many) - 1) == -6 and sort(many, ws=A16 + 8) == -5
+    for f in (lambda **k: move("mx_route_gather", **k), lambda **k: move("mx_route_gather_bwd", **k)):
+        assert f(d=None) == -1 and f(a=None) == -1 and f(b=None) == -1 and f(rows=None) == -1
+        assert f(d=rd(features=0)) == -2 and f(lda=99) == -2 and f(ldb=99) == -2 and f(dt=3) == -3
+        assert f(a=A16 + 1) == -5 and f(b=A16 + 1) == -5 and f(rows=A16 + 2) == -5
+    assert combine(None) == -1 and combine(y=None) == -1 and combine(rows=None) == -1 and combine(w=None) == -1 and combine(out=None) == -1
+    assert combine(dt=7) == -3 and combine(ldy=99) == -2 and combine(ldo=99) == -2 and combine(w=A16 + 2) == -5
+    assert combine(y=A16 + 1) == -5 and combine(out=A16 + 1) == -5
+    assert combine_bwd(None) == -1 and combine_bwd(dout=None) == -1 and combine_bwd(y=None) == -1 and combine_bwd(w=None) == -1
+    assert combine_bwd(dy=None, dw=None) == -1 and combine_bwd(rows=None) == -1
+    assert combine_bwd(lddy=99) == -2 and combine_bwd(dy=A16 + 1) == -5 and combine_bwd(dw=A16 + 2) == -5 and combine_bwd(dt=-1) == -3
+    # no tokens: nothing runs
+    none = rd(tokens=0)
+    assert move("mx_route_gather", none, a=None, b=None, rows=None) == 0 and combine(none, None, rows=None, w=None, out=None) == 0
+    assert combine_bwd(none, None, y=None, rows=None, w=None, dy=None, dw=None) == 0
+
+
+def test_binding_rejects_unusable_tensors():
+    d, x, w = mx.norm_desc(**ND), torch.zeros(10, 100), torch.ones(100)
+    with pytest.raises(ValueError, match="float32, bfloat16 or float16"):
+        mx.mx_norm_fwd(d, x.double(), w, x)
+    with pytest.raises(ValueError, match="shape"):
+        mx.mx_norm_fwd(d, x[:9], w, x)
+    with pytest.raises(ValueError, match="device memory"):
+        mx.mx_norm_fwd(d, x, w, x)
+    r, idx, wt = rd(), torch.zeros(10, 2, dtype=torch.int32), torch.zeros(10, 2)
+    with pytest.raises(ValueError, match="int32"):
+        mx.mx_route_sort(r, idx.long(), None, None)
+    with pytest.raises(ValueError, match="values"):
+        mx.mx_route_sort(r, idx[:9], None, None)
+    with pytest.raises(TypeError):
+        mx.mx_route_sort(r, [1, 2], None, None)
+    with pytest.raises(ValueError, match="device memory"):
+        mx.mx_route_sort(r, idx, None, None)
+    with pytest.raises(ValueError, match="shape"):
+        mx.mx_route_combine(r, x, idx, wt, x[:9])
+
+
+def test_types_that_must_agree(monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    d, x, w = mx.norm_desc(**ND), torch.zeros(10, 100), torch.ones(100)
+    with pytest.raises(ValueError, match="x's type"):
+        mx.mx_norm_fwd(d, x, w, residual=x.half())
+    with pytest.raises(ValueError, match="x's type"):
+        mx.mx_norm_fwd(d, x, w, total=x.bfloat16())
+    with pytest.raises(ValueError, match="100 contiguous"):
+        mx.mx_norm_fwd(d, x, torch.ones(200)[::2], x)
+    with pytest.raises(ValueError, match="float32"):
+        mx.mx_norm_fwd(d, x, w, x, rstd=torch.ones(10).half())
+    with pytest.raises(ValueError, match="total's type"):
+        mx.mx_norm_bwd(d, x, x, w, torch.ones(10), x.half())
+    with pytest.raises(TypeError, match="Linear8QTensor"):
+        mx.mx_norm_fwd(d, x, w, yq=mx.LinearQTensor(mx.linear_desc(10, 8, 100), 0, "cpu"))
+    r, rows, idx = rd(), torch.zeros(20, 100), torch.zeros(10, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="type"):
+        mx.mx_route_gather(r, x, idx, rows.half())
+    with pytest.raises(ValueError, match="type"):
+        mx.mx_route_combine_bwd(r, x, rows, idx, torch.zeros(10, 2), rows.half())
+    with pytest.raises(ValueError, match="float32"):
+        mx.mx_route_combine(r, rows, idx, torch.zeros(10, 2).half(), x)
+
+
+CALLS = {"norm_fwd": ("x", "weight", "y", "residual", "total", "yq", "rstd"),
+         "norm_bwd": ("dy", "total", "weight", "rstd", "dx", "dweight", "dtotal", "ws"),
+         "route_sort": ("expert", "offsets", "rows", "order", "ws"), "route_gather": ("x", "rows", "out"),
+         "route_gather_bwd": ("dout", "rows", "dx"), "route_combine": ("y", "rows", "weight", "out"),
+         "route_combine_bwd": ("dout", "y", "rows", "weight", "dy", "dweight")}
+
+
+@pytest.fixture
+def reached(monkeypatch):
+    """The calls that reach the library; the current device is 0, its stream 0x1000."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            real = getattr(mx.lib(), name)
+            return real if name.endswith("_bytes") else lambda *a: calls.append((name, a[-1])) or 0
+    for m in (MN, MR):
+        m._load()
+        monkeypatch.setattr(m, "_lib", Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x1000 + d, raising=False)
+    for name in ("_current_device", "_current_stream"):
+        monkeypatch.setattr(mx, name, None, raising=False)
+    return calls
+
+
+def run(call, where, stream=None):
+    """`call` with each argument on the device that where(argument) gives."""
+    m, c, e, k = 10, 2, 4, 100
+    nd, r = mx.norm_desc(m, k), mx.route_desc(m, c, e, k)
+
+    def t(name, *shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(on(where(name)))
+
+    def i(name, *shape):
+        return t(name, *shape, dtype=torch.int32)
+
+    def q(name):
+        v = mx.Linear8QTensor(mx.linear_desc(m, 8, k, block=1), 0, "cpu")
+        v.is_cuda, v.device_index = True, where(name)
+        return v
+    {"norm_fwd": lambda: mx.mx_norm_fwd(nd, t("x", m, k), t("weight", k), t("y", m, k), t("residual", m, k), t("total", m, k), q("yq"),
+                                        t("rstd", m), stream),
+     "norm_bwd": lambda: mx.mx_norm_bwd(nd, t("dy", m, k), t("total", m, k), t("weight", k), t("rstd", m), t("dx", m, k), t("dweight", k),
+                                        t("dtotal", m, k), t("ws", 4096), stream),
+     "route_sort": lambda: mx.mx_route_sort(r, i("expert", m, c), i("offsets", e + 1), i("rows", m, c), i("order", m * c), t("ws", 64), stream),
+     "route_gather": lambda: mx.mx_route_gather(r, t("x", m, k), i("rows", m, c), t("out", m * c, k), stream),
+     "route_gather_bwd": lambda: mx.mx_route_gather_bwd(r, t("dout", m * c, k), i("rows", m, c), t("dx", m, k), stream),
+     "route_combine": lambda: mx.mx_route_combine(r, t("y", m * c, k), i("rows", m, c), t("weight", m, c), t("out", m, k), stream),
+     "route_combine_bwd": lambda: mx.mx_route_combine_bwd(r, t("dout", m, k), t("y", m * c, k), i("rows", m, c), t("weight", m, c),
+                                                          t("dy", m * c, k), t("dweight", m, c), stream)}[call]()
+
+
+@pytest.mark.parametrize("call,odd", [(c, a) for c, args in CALLS.items() for a in args])
+def test_one_tensor_on_another_device(reached, call, odd):
+    for stream in (None, 0, 0x7000, Stream(0)):
+        with pytest.raises(ValueError, match="device"):
+            run(call, lambda name: int(name == odd), stream)
+    assert not reached
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_tensors_on_the_streams_device_pass(reached, call):
+    for device, stream, handle in ((0, None, 0x1000), (0, 0, 0), (0, Stream(0), 0x5000), (1, Stream(1), 0x5000), (1, 0x7000, 0x7000)):
+        run(call, lambda name: device, stream)
+        (name, got), = reached
+        assert name == "mx_" + call and got == handle
+        reached.clear()

@@ -143,7 +143,7 @@ def test_tensors_in_4_and_8_bits_are_told_apart():
     d4, d8 = mx.linear_desc(**GOOD), mx.linear_desc(**D8)
     q4, q8 = mx.LinearQTensor(d4, 0, "cpu"), mx.Linear8QTensor(d8, 0, "cpu")
     with pytest.raises(TypeError, match="Linear8QTensor"):
-        mx.mx_linear8_fwd(d8, mx.Linear8QTensor(d8, 1, "cpu"), q4, None)
+        mx.mx_linear8_fwd(d8, q4, q8, None)
     with pytest.raises(TypeError, match="LinearQTensor"):
         mx.mx_linear_fwd(d4, q8, q4, None)
     # one made for a block size serves the other
