@@ -25,7 +25,7 @@ SOURCES = ["capi.cpp", "quantize.hip", "quantize_mx.hip", "conv.hip", "conv_stag
 # the linear layers and the gradient clip (the measured traffic of the conv
 # kernels is filed under the hash of csrc/ alone)
 LINEAR_SOURCES = ["linear_capi.cpp", "linear_quant.hip", "linear_gemm.hip", "linear_few.hip", "grad_clip.hip",
-                  "linear8_capi.cpp", "linear8_quant.hip", "linear8_gemm.hip", "layer_capi.cpp", "norm.hip", "route.hip"]
+                  "linear8_capi.cpp", "linear8_quant.hip", "linear8_gemm.hip", "linear8_few.hip", "layer_capi.cpp", "norm.hip", "route.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++20", "-fPIC", "-ffp-contract=off",

@@ -29,5 +29,18 @@ size_t lin8_product_workspace(const LinGeom& g, LinOp op);
 hipError_t launch_lin8_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
                                void* out, mx_dtype dtype, int64_t ld, const int32_t* offsets, void* workspace,
                                hipStream_t s);
+// fwd and dgrad with few tokens, where lin8_few() says so.
+bool lin8_few(const LinGeom& g);
+hipError_t launch_lin8_few(const LinGeom& g, bool dgrad, const mx_linear_qtensor* wq, const mx_linear_qtensor* xq, void* y,
+                           mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s);
+// Quantize-and-multiply in one launch, where lin8_fused() says so.
+bool lin8_fused(const LinGeom& g);
+hipError_t launch_lin8_fused(const LinGeom& g, const mx_linear_qtensor* wq, const void* x, mx_dtype x_dtype, int64_t ldx,
+                             void* y, mx_dtype y_dtype, int64_t ldy, const int32_t* offsets, hipStream_t s);
+
+// What a call launches, for the tests (linear.h's LinVariant).
+LinVariant lin8_product_variant(const LinGeom& g, LinOp op, mx_dtype dtype);
+bool lin8_product_streams(const LinGeom& g, LinOp op, const void* out, mx_dtype dtype, int64_t ld);
+LinVariant lin8_few_variant(const LinGeom& g, bool dgrad, bool fused);
 
 }  // namespace mx

@@ -12,7 +12,7 @@ using namespace mx;
 size_t apply_code_bytes(const LinGeom& g) { return static_cast<size_t>(g.mp / kTileR * (g.kp / kTileC)) * k8TileBytes; }
 size_t apply_scale_bytes(const LinGeom& g) { return static_cast<size_t>(g.mp / kPad * (g.kp / kPad)) * k8ScaleBytes; }
 size_t apply_workspace(const LinGeom& g) {
-  if (g.m == 0) return 0;
+  if (g.m == 0 || lin8_fused(g)) return 0;
   return apply_code_bytes(g) + apply_scale_bytes(g) + lin8_product_workspace(g, LIN_FWD);
 }
 
@@ -123,11 +123,30 @@ mx_status mx_linear8_apply(const mx_linear_desc* desc, const mx_linear_qtensor* 
   if ((st = check_offsets(g, offsets)) != MX_OK) return st;
   if ((st = check_workspace(workspace, ws_bytes, apply_workspace(g))) != MX_OK) return st;
   if (g.m == 0) return MX_OK;
+  if (lin8_fused(g)) return launched(launch_lin8_fused(g, wq, x, x_dtype, ldx, y, y_dtype, ldy, offsets, stream));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const mx_linear_qtensor xq{ws, ws + apply_code_bytes(g), nullptr, nullptr};
   const hipError_t e = launch_lin8_quantize(g, MX_ROLE_ACT, 1, x, x_dtype, ldx, offsets, &xq, stream);
   if (e != hipSuccess) return MX_ERR_LAUNCH;
   return launched(launch_lin8_product(g, LIN_FWD, &xq, wq, y, y_dtype, ldy, offsets, ws + apply_code_bytes(g) + apply_scale_bytes(g), stream));
+}
+
+// Not part of the ABI: mx_internal_linear_variant of the layers in 8 bits, which
+// depends on the output's type.
+mx_status mx_internal_linear8_variant(const mx_linear_desc* desc, int call, mx_dtype dtype, int64_t* out) {
+  const mx_status st = check_desc(desc, kPad);
+  if (st != MX_OK) return st;
+  if (!out) return MX_ERR_NULL;
+  const LinGeom g = make_lin_geom(desc);
+  const LinVariant v = call == 3 && g.m > 0 && lin8_fused(g)
+                           ? lin8_few_variant(g, false, true)
+                           : lin8_product_variant(g, call == 1 ? LIN_DGRAD : call == 2 ? LIN_WGRAD : LIN_FWD, dtype);
+  out[0] = v.kernel;
+  out[1] = v.size;
+  out[2] = v.splits;
+  out[3] = v.threads;
+  out[4] = v.workgroups;
+  return MX_OK;
 }
 
 }  // extern "C"

@@ -15,8 +15,9 @@
 // them (EXACT) the codes are widened to bf16, scales included, and go to the
 // bf16 MFMA, whose products are exact and whose sums are fp32, at half the rate.
 //
-// A wave takes 64 x 64 outputs and loads its operands from memory into the
-// registers that the MFMA reads, as they are stored.
+// Operands go from memory to LDS as they are stored, without passing registers,
+// several slices of 64 columns ahead, and from there to the registers that the
+// MFMA reads, one slice ahead.
 #include "linear8_codes.h"
 #include "linear_product.h"
 
@@ -26,23 +27,92 @@
 namespace mx {
 namespace {
 
-using Plain = Shape<128, 128, 2, 2, 1>;
+// Big for the MFMA's rate, Tiny for short latency (make_plan).
+using Big = Shape<256, 256, 2, 2, 4>;
+using Small = Shape<128, 128, 2, 2, 4>;
+using Tiny = Shape<64, 64, 2, 2, 4>;
 
+// Copies 16 (or 4) bytes per lane from src + off to the LDS address dst + lane *
+// 16 (4) without passing registers.  src and dst are the wave's.  The compiler
+// does not know of the copy (told of it, it would wait for all copies on
+// their way before any LDS read), so whoever reads the data waits for it with
+// wait_barrier.  There is no output register, and the address registers are
+// read when the instruction issues.  The LDS address goes in m0, which is an
+// operand, so that the compiler writes it and knows of it (and an instruction
+// has to pass between that write and the copy).
+__device__ __forceinline__ void copy16_lds(const uint8_t* src, uint32_t off, uint32_t dst) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "{m0}"(dst), "v"(off), "s"(src) : "memory");
+}
+__device__ __forceinline__ void copy4_lds(const uint8_t* src, uint32_t off, uint32_t dst) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" : : "{m0}"(dst), "v"(off), "s"(src) : "memory");
+}
+
+// TM x TN outputs per workgroup, by WM x WN waves in MFMAs of 32x32x64, or
+// (EXACT) 32x32x16 on the widened operands.  One step contracts a slice of 64
+// columns.  A tile's plane in LDS is read as it is, 64 lanes x 16 consecutive
+// bytes, which is free of bank conflicts.
 template <class T, class Shape, bool CONTRACT, bool EXACT>
 __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(const ProductParams p) {
-  constexpr int TM = Shape::TM, TN = Shape::TN, WM = Shape::WM, WN = Shape::WN;
-  constexpr int RM = TM / WM / 32, RN = TN / WN / 32;
-  static_assert(TM == kPad && TN == kPad);
-  __shared__ __attribute__((aligned(16))) uint8_t lds[WM * WN * store_bytes<T, RN>()];
+  constexpr int TM = Shape::TM, TN = Shape::TN, WM = Shape::WM, WN = Shape::WN, kStages = Shape::kStages;
+  constexpr int RM = TM / WM / 32, RN = TN / WN / 32;  // MFMA rows and columns of a wave
+  constexpr int kWaves = WM * WN;
+  constexpr int kOpndA = TM / 32 * k8TileBytes, kOpndB = TN / 32 * k8TileBytes;
+  // groups of 128 rows' scales (of which a tile of 64 uses half), each there twice: for lanes 0..31 and 32..63
+  constexpr int kGroupsA = (TM + kPad - 1) / kPad, kGroups = kGroupsA + (TN + kPad - 1) / kPad;
+  constexpr int kGroupBytes = 2 * k8ScaleBytes;
+  constexpr int kScales = kOpndA + kOpndB;  // their place in a stage
+  constexpr int kStage = kScales + kGroups * kGroupBytes;
+  constexpr int kStoreBytes = kWaves * store_bytes<T, RN>();
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage > kStoreBytes ? kStages * kStage : kStoreBytes];
+
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
   Work w;
   if (!find_work<TM, TN, CONTRACT>(p, w)) return;
-  const uint8_t* a = p.a + ((w.arow / kTileR + wm * RM) * p.akt + w.k0) * k8TileBytes;
-  const uint8_t* b = p.b + ((w.brow / kTileR + wn * RN) * p.bkt + w.k0) * k8TileBytes;
-  const uint8_t* as = p.as + (w.arow / kPad * (p.akt / 2) + w.k0 / 2) * k8ScaleBytes;
-  const uint8_t* bs = p.bs + (w.brow / kPad * (p.bkt / 2) + w.k0 / 2) * k8ScaleBytes;
+  const int nslices = 2 * w.nsteps;
+
+  // Copies of a slice: copy l of wave w takes plane l * kWaves + w of a's tiles,
+  // then of b's, and then groups of scales.  A stripe past the operand's end is
+  // read as its last one: those outputs are not stored.
+  constexpr int kPlanesA = TM / 16 / kWaves, kPlanes = (TM + TN) / 16 / kWaves;
+  constexpr int kScaleCopies = (kGroups + kWaves - 1) / kWaves, kCopies = kPlanes + kScaleCopies;
+  static_assert(TM / 16 % kWaves == 0 && TN / 16 % kWaves == 0);
+  const uint8_t *src[kPlanes], *ssrc[kScaleCopies];
+  uint32_t sdst[kScaleCopies];
+  static_for<kPlanes>([&](auto lc) {
+    constexpr int L = decltype(lc)::value;
+    constexpr bool of_b = L >= kPlanesA;
+    const int i = (of_b ? L - kPlanesA : L) * kWaves + wave;
+    const int64_t st = min((of_b ? w.brow : w.arow) / kTileR + i / 2, (of_b ? p.b_rows : p.a_rows) / kTileR - 1);
+    src[L] = (of_b ? p.b : p.a) + (st * (of_b ? p.bkt : p.akt) + w.k0) * k8TileBytes + i % 2 * 1024;
+  });
+  static_for<kScaleCopies>([&](auto lc) {
+    constexpr int L = decltype(lc)::value;
+    const int i = min(L * kWaves + wave, kGroups - 1);  // (the last group may be copied twice)
+    const bool of_b = i >= kGroupsA;
+    const int64_t g = min((of_b ? w.brow : w.arow) / kPad + (of_b ? i - kGroupsA : i), (of_b ? p.b_rows : p.a_rows) / kPad - 1);
+    ssrc[L] = (of_b ? p.bs : p.as) + (g * ((of_b ? p.bkt : p.akt) / 2) + w.k0 / 2) * k8ScaleBytes;
+    sdst[L] = kScales + static_cast<uint32_t>(i) * kGroupBytes;
+  });
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  // copy l of the slice that the sources stand at, into the stage at `to`
+  auto copy = [&](uint32_t to, auto l) {
+    constexpr int L = decltype(l)::value;
+    if constexpr (L < kPlanes) copy16_lds(src[L], lane * 16u, lds0 + to + (L * kWaves + wave) * 1024);
+    else copy4_lds(ssrc[L - kPlanes], (lane & 31) * 4u, lds0 + to + sdst[L - kPlanes]);
+  };
+  // to the next slice; two share their scales
+  auto advance = [&](bool on, bool odd) {
+    const int d = on ? 1 : 0;
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) src[q] += d * k8TileBytes;
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < kScaleCopies; ++i) ssrc[i] += d * k8ScaleBytes;
+    }
+  };
+
   f32x16 acc[RM][RN];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
@@ -50,51 +120,212 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(con
     for (int j = 0; j < RN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  for (int s = 0; s < w.nsteps; ++s) {
-    const uint32_t sa = reinterpret_cast<const uint32_t*>(as + static_cast<int64_t>(s) * k8ScaleBytes)[lane & 31] >> (8 * RM * wm);
-    const uint32_t sb = reinterpret_cast<const uint32_t*>(bs + static_cast<int64_t>(s) * k8ScaleBytes)[lane & 31] >> (8 * RN * wn);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      auto load = [&](const uint8_t* src, int64_t kt, int i) {
-        const i32x4* q = reinterpret_cast<const i32x4*>(src + (i * kt + 2 * s + t) * k8TileBytes);
-        const i32x4 lo = q[lane], hi = q[64 + lane];
-        return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      };
-      i32x8 fa[RM], fb[RN];
-#pragma unroll
-      for (int i = 0; i < RM; ++i) fa[i] = load(a, p.akt, i);
-#pragma unroll
-      for (int j = 0; j < RN; ++j) fb[j] = load(b, p.bkt, j);
-      if constexpr (EXACT) {
-        Wide wa[RM], wb[RN];
-#pragma unroll
-        for (int i = 0; i < RM; ++i) wa[i] = widen(fa[i], sa, i);
-#pragma unroll
-        for (int j = 0; j < RN; ++j) wb[j] = widen(fb[j], sb, j);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < RM; ++i)
-#pragma unroll
-            for (int j = 0; j < RN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j].k[q], wa[i].k[q], acc[i][j], 0, 0, 0);
-      } else static_for<RM * RN>([&](auto n) {
+
+  struct Frags {
+    i32x4 a[RM][2], b[RN][2];
+    int sa, sb;
+  };
+  Frags fA, fB;
+  // a wave's scales: the bytes of its 1, 2 or 4 stripes among 128 rows' four
+  auto read_scales = [&](const uint8_t* s, int stripe, int n) -> int {
+    const uint8_t* at = s + (stripe >> 2) * kGroupBytes + 4 * lane + (stripe & 3);
+    return n == 4 ? *reinterpret_cast<const int*>(at) : n == 2 ? *reinterpret_cast<const uint16_t*>(at) : *at;
+  };
+  // (the tile's first stripe among its 128 rows' four)
+  const int sa0 = TM < kPad ? static_cast<int>(w.arow / kTileR & 3) : 0, sb0 = TN < kPad ? static_cast<int>(w.brow / kTileR & 3) : 0;
+  constexpr int kReads = 2 * (RM + RN) + 2;
+  auto read = [&](const uint8_t* st, Frags& f, auto r) {
+    constexpr int R = decltype(r)::value;
+    if constexpr (R == 0) {
+      f.sa = read_scales(st + kScales, sa0 + wm * RM, RM);
+    } else if constexpr (R == 1) {
+      f.sb = read_scales(st + kScales + kGroupsA * kGroupBytes, sb0 + wn * RN, RN);
+    } else if constexpr (R < 2 + 2 * RM) {
+      constexpr int I = (R - 2) / 2, P = (R - 2) % 2;
+      f.a[I][P] = reinterpret_cast<const i32x4*>(st + (wm * RM + I) * k8TileBytes + P * 1024)[lane];
+    } else {
+      constexpr int I = (R - 2 - 2 * RM) / 2, P = (R - 2) % 2;
+      f.b[I][P] = reinterpret_cast<const i32x4*>(st + kOpndA + (wn * RN + I) * k8TileBytes + P * 1024)[lane];
+    }
+  };
+  auto both = [](const i32x4 (&v)[2]) {
+    return i32x8{v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  };
+
+  // items dealt out evenly over the first `span` MFMAs of a slice: those that follow MFMA n
+  auto deal = [&](auto n, auto count, auto span, auto&& f) {
+    constexpr int N = decltype(n)::value, C = decltype(count)::value, S = decltype(span)::value;
+    constexpr int B = N < S ? (N * C + S - 1) / S : C, E = N + 1 < S ? ((N + 1) * C + S - 1) / S : C;
+    static_for<E - B>([&](auto i) { f(Idx<B + decltype(i)::value>{}); });
+  };
+  // EXACT: the operands of one of a slice's four steps of 16 columns
+  struct Step { bf16x8 a[RM], b[RN]; };
+  auto scale = [](int s, int i) { return __uint_as_float((static_cast<uint32_t>(s) >> (8 * i) & 0xFFu) << 23); };
+  auto convert = [&](const Frags& f, Step& x, auto q, auto i) {
+    constexpr int Q = decltype(q)::value, I = decltype(i)::value;
+    if constexpr (I < RM) x.a[I] = widen8(f.a[I][Q / 2][Q % 2 * 2], f.a[I][Q / 2][Q % 2 * 2 + 1], scale(f.sa, I));
+    else x.b[I - RM] = widen8(f.b[I - RM][Q / 2][Q % 2 * 2], f.b[I - RM][Q / 2][Q % 2 * 2 + 1], scale(f.sb, I - RM));
+  };
+  Step x0, x1;
+  // multiplies the slice in f; extra(n, total) follows MFMA n of total
+  constexpr int kSlots = RM * RN * (EXACT ? 4 : 1);
+  auto multiply = [&](const Frags& f, auto&& extra) {
+    if constexpr (EXACT) {
+      static_for<RM + RN>([&](auto i) { convert(f, x0, Idx<0>{}, i); });
+      static_for<4>([&](auto q) {
+        constexpr int Q = decltype(q)::value;
+        const Step& now = Q % 2 ? x1 : x0;
+        Step& next = Q % 2 ? x0 : x1;
+        static_for<RM * RN>([&](auto n) {
+          constexpr int N = decltype(n)::value, I = N / RN, J = N % RN;
+          acc[I][J] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.b[J], now.a[I], acc[I][J], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (Q < 3) deal(n, Idx<RM + RN>{}, Idx<RM * RN>{}, [&](auto i) { convert(f, next, Idx<Q + 1>{}, i); });
+          extra(Idx<Q * RM * RN + N>{});
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    } else {
+      static_for<RM * RN>([&](auto n) {
         constexpr int I = decltype(n)::value / RN, J = decltype(n)::value % RN;
-        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[J], fa[I], acc[I][J], 0, 0, J, static_cast<int>(sb), I, static_cast<int>(sa));
+        acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(both(f.b[J]), both(f.a[I]), acc[I][J], 0, 0, J, f.sb, I, f.sa);
+        __builtin_amdgcn_sched_barrier(0);
+        extra(n);
+        __builtin_amdgcn_sched_barrier(0);
       });
     }
+  };
+
+  // Slice s, on stage s%S of S, with its operands read during slice s-1:
+  //   multiply it, reading slice s+1 from its stage and copying slice s+S into
+  //   stage s%S, which every wave had read at the last barrier;
+  //   barrier: every wave has read slice s+1, and its copies of slice s+2 have
+  //   arrived (those of the S-2 slices after may be on their way).
+  // With one wave per SIMD nothing else hides an LDS access, so reads and
+  // copies are dealt out between the MFMAs.  Copies past the last slice repeat
+  // it, into stages that nothing reads.
+  if (nslices > 0) {
+    static_for<kStages>([&](auto st) {
+      constexpr int S = decltype(st)::value;
+      static_for<kCopies>([&](auto l) { copy(S * kStage, l); });
+      advance(S + 1 < nslices, S % 2);
+    });
+    wait_barrier<(kStages - 2) * kCopies>();
+    static_for<kReads>([&](auto r) {
+      read(lds, fA, r);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // (all have read slice 0: its stage is copied into from here on)
+    wait_barrier<(kStages - 2) * kCopies>();
+    static_assert(kStages % 2 == 0);
+    uint32_t cur = 0;
+    auto slice = [&](const Frags& f, Frags& g, int s, bool odd) {
+      const uint32_t next = cur == (kStages - 1) * kStage ? 0 : cur + kStage;
+      multiply(f, [&](auto n) {
+        deal(n, Idx<kReads>{}, Idx<(kSlots * 3 + 3) / 4>{}, [&](auto r) { read(lds + next, g, r); });
+        deal(n, Idx<kCopies>{}, Idx<kSlots>{}, [&](auto l) { copy(cur, l); });
+      });
+      advance(s + kStages + 1 < nslices, odd);
+      wait_barrier<(kStages - 2) * kCopies>();
+      cur = next;
+    };
+    for (int s = 0; s < nslices; s += 2) {
+      slice(fA, fB, s, false);
+      slice(fB, fA, s + 1, true);
+    }
+    // the last copies have to land before the stores reuse LDS
+    wait_barrier<0>();
   }
+
   T* tile = static_cast<T*>(p.out) + w.out + w.orow * p.ld + static_cast<int64_t>(w.tj) * TN;
-  store_wave<false, RM, RN>(acc, lds + wave * store_bytes<T, RN>(), tile, p.ld, w.rleft, w.cleft, lane, wm, wn);
+  uint8_t* buf = lds + wave * store_bytes<T, RN>();
+  if (p.stream) store_wave<true, RM, RN>(acc, buf, tile, p.ld, w.rleft, w.cleft, lane, wm, wn);
+  else store_wave<false, RM, RN>(acc, buf, tile, p.ld, w.rleft, w.cleft, lane, wm, wn);
+}
+
+struct Plan {
+  int shape;    // 0: Tiny, 1: Small, 2: Big
+  int64_t tiles_i, tiles_j;
+  int splits, split_steps;
+  int64_t units;  // workgroups, at most
+};
+
+LinVariant variant(const Plan& pl) {
+  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny::TM;
+  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : Tiny::kThreads;
+  return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
+}
+
+Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
+  const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
+  const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
+  const int64_t used = g.m < g.ew ? g.m : g.ew;
+  // steps of a tile, of 128 columns: with experts, wgrad contracts one's share of the tokens
+  const int64_t all_steps = contract / kPad;
+  const double steps = op == LIN_WGRAD ? static_cast<double>(all_steps) / g.ew : static_cast<double>(all_steps);
+  Plan best{};
+  double best_time = 0.0;
+  auto consider = [&](int shape, int64_t pieces) {
+    Plan pl{};
+    const int tm = shape == 2 ? Big::TM : shape == 1 ? Small::TM : Tiny::TM, tn = shape == 2 ? Big::TN : shape == 1 ? Small::TN : Tiny::TN;
+    // every expert with tokens may leave a part of a tile more
+    const int64_t extra = op != LIN_WGRAD && g.e > 0 ? used : 0;
+    pl.shape = shape;
+    pl.tiles_i = (rows + tm - 1) / tm + extra;
+    pl.tiles_j = (cols + tn - 1) / tn;
+    pl.units = pl.tiles_i * pl.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
+    pl.split_steps = static_cast<int>((all_steps + pieces - 1) / pieces);
+    pl.splits = pieces > 1 ? static_cast<int>((all_steps + pl.split_steps - 1) / pl.split_steps) : 1;
+    const int64_t likely = pl.units - extra * pl.tiles_j / 2;
+    const double rounds = static_cast<double>((likely * pl.splits + 255) / 256), each = steps / pl.splits * (exact ? 2 : 1);
+    double time = shape == 2 ? rounds * (9.0 + 1.4 * each) : shape == 1 ? 5.0 + rounds * 0.5 * each : 3.6 + rounds * 0.24 * each;
+    if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
+    const LinVariant v = variant(pl);
+    if (v.workgroups * v.threads > std::numeric_limits<uint32_t>::max()) return;
+    if (best.units == 0 || time < best_time) {
+      best = pl;
+      best_time = time;
+    }
+  };
+  for (int shape : {0, 1, 2}) consider(shape, 1);
+  if (g.e == 0)
+    for (int64_t s = 2; s <= 16 && 4 * s <= all_steps; s *= 2) consider(0, s);
+  return best;
 }
 
 }  // namespace
 
-size_t lin8_product_workspace(const LinGeom& g, LinOp op) { return 0; }
+LinVariant lin8_product_variant(const LinGeom& g, LinOp op, mx_dtype dtype) {
+  if (op != LIN_WGRAD && g.m == 0) return {};
+  if (op != LIN_WGRAD && lin8_few(g)) return lin8_few_variant(g, op == LIN_DGRAD, false);
+  return variant(make_plan(g, op, dtype == MX_F32));
+}
+
+// Whether the product writes past the caches: the rule of the products in 4
+// bits.
+bool lin8_product_streams(const LinGeom& g, LinOp op, const void* out, mx_dtype dtype, int64_t ld) {
+  return lin_product_streams(g, op, out, dtype, ld);
+}
+
+size_t lin8_product_workspace(const LinGeom& g, LinOp op) {
+  if (g.m == 0 || (op != LIN_WGRAD && lin8_few(g))) return 0;
+  size_t need = 0;
+  for (bool exact : {false, true}) {
+    const Plan pl = make_plan(g, op, exact);
+    if (pl.splits <= 1) continue;
+    const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
+    const size_t b = static_cast<size_t>(pl.splits * rows * ((cols + 3) / 4 * 4)) * sizeof(float);
+    need = b > need ? b : need;
+  }
+  return need;
+}
 
 hipError_t launch_lin8_product(const LinGeom& g, LinOp op, const mx_linear_qtensor* aq, const mx_linear_qtensor* bq,
                                void* out, mx_dtype dtype, int64_t ld, const int32_t* offsets, void* workspace,
                                hipStream_t s) {
   if (op != LIN_WGRAD && g.m == 0) return hipSuccess;
+  if (op != LIN_WGRAD && lin8_few(g)) return launch_lin8_few(g, op == LIN_DGRAD, bq, aq, out, dtype, ld, offsets, s);
+  const Plan pl = make_plan(g, op, dtype == MX_F32);
   ProductParams p{};
   const mx_role ra = op == LIN_FWD ? MX_ROLE_ACT : MX_ROLE_GRAD, rb = op == LIN_WGRAD ? MX_ROLE_ACT : MX_ROLE_WEIGHT;
   const mx_form fa = op == LIN_WGRAD ? MX_FORM_COLS : MX_FORM_ROWS, fb = op == LIN_FWD ? MX_FORM_ROWS : MX_FORM_COLS;
@@ -111,21 +342,48 @@ hipError_t launch_lin8_product(const LinGeom& g, LinOp op, const mx_linear_qtens
   p.b_rows = p.bmat * form_matrices(g, rb);
   p.rows = op == LIN_WGRAD ? g.n : g.m;
   p.cols = op == LIN_FWD ? g.n : g.k;
-  p.out = out;
-  p.ld = ld;
+  // a split product leaves fp32 sums in the workspace, with rows of whole 16
+  // bytes, for k_lin_reduce
+  const bool split = pl.splits > 1;
+  const int64_t pcols = (p.cols + 3) / 4 * 4;
+  p.out = split ? workspace : out;
+  p.ld = split ? pcols : ld;
+  p.split_out = p.rows * pcols;
+  p.stream = !split && lin8_product_streams(g, op, out, dtype, ld);
   p.tokens = static_cast<int>(g.m);
   p.offsets = offsets;
   p.experts = g.e;
-  const int64_t used = g.m < g.ew ? g.m : g.ew;
-  p.tiles_i = static_cast<int>((p.rows + kPad - 1) / kPad + (op != LIN_WGRAD && g.e > 0 ? used : 0));
-  p.tiles_j = static_cast<int>((p.cols + kPad - 1) / kPad);
-  p.splits = 1;
-  const int64_t units = static_cast<int64_t>(p.tiles_i) * p.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
+  p.tiles_i = static_cast<int>(pl.tiles_i);
+  p.tiles_j = static_cast<int>(pl.tiles_j);
+  p.splits = pl.splits;
+  p.split_steps = pl.split_steps;
+  const LinVariant v = variant(pl);
+  // out's type, and whether the products are exact
+  auto multiply = [&](auto t, auto exact) {
+    using T = decltype(t);
+    constexpr bool X = decltype(exact)::value;
+    auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(v.workgroups)), dim3(v.threads), 0, s, p); };
+    auto with = [&](auto contract) {
+      constexpr bool C = decltype(contract)::value;
+      pl.shape == 2 ? launch(k_lin8_product<T, Big, C, X>) : pl.shape == 1 ? launch(k_lin8_product<T, Small, C, X>) : launch(k_lin8_product<T, Tiny, C, X>);
+    };
+    op == LIN_WGRAD ? with(std::true_type{}) : with(std::false_type{});
+  };
+  auto reduce = [&](auto t) {
+    using T = decltype(t);
+    const int64_t n = p.rows * pcols / 4;
+    const unsigned wgs = static_cast<unsigned>(n / 256 < 2048 ? (n + 255) / 256 : 2048);
+    hipLaunchKernelGGL(k_lin_reduce<T>, dim3(wgs), dim3(256), 0, s, static_cast<const float*>(workspace), p.splits, p.rows, p.cols, pcols,
+                       static_cast<T*>(out), ld);
+  };
   auto go = [&](auto t) {
     using T = decltype(t);
-    auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((units + 7) / 8 * 8)), dim3(Plain::kThreads), 0, s, p); };
-    constexpr bool X = std::is_same_v<T, float>;
-    op == LIN_WGRAD ? launch(k_lin8_product<T, Plain, true, X>) : launch(k_lin8_product<T, Plain, false, X>);
+    using X = std::bool_constant<std::is_same_v<T, float>>;
+    if (!split) multiply(t, X{});
+    else {
+      multiply(float{}, X{});
+      reduce(t);
+    }
   };
   switch (dtype) {
     case MX_BF16: go(bf16_t{}); break;

@@ -20,49 +20,13 @@
 // us and 256 tokens of 64 experts 42.
 #include <type_traits>
 
-#include "linear.h"
 #include "linear_codes.h"
+#include "linear_few.h"
 
 namespace mx {
 namespace {
 
-constexpr int kMaxWaves = 8;
 constexpr size_t kTokenLds = size_t{48} << 10;  // for a pass' codes and scales: three workgroups share a CU where there are that many
-constexpr int kSumStride = 33;                  // words per token of a wave's sums: no bank conflicts
-
-struct FewParams {
-  const uint8_t *w, *ws;
-  int64_t kt;              // column tiles of a stripe
-  int64_t mat_stripes;     // of one expert's matrix
-  const void* x;           // unquantized tokens, or their codes
-  const uint8_t* xs;       // the codes' scales
-  int64_t ldx;
-  void* y;
-  int64_t ldy;
-  int y_dtype;
-  int tokens, n, k;
-  const int32_t* offsets;
-  int experts;
-  int per_pass;            // tokens of a pass, 32 at most
-  int passes;              // of all experts, at most
-  int whole;               // whether an XCD takes all stripes of a pass, else an eighth
-  int part;                // groups of SN stripes that it takes
-};
-
-// The lane's piece of what starts at p, an address that the wave has in common.
-// (The empty asm keeps the compiler from adding the lane's part first, which
-// would cost a pair of vector registers for each of these loads.)
-template <class T>
-__device__ __forceinline__ T lane_load(const uint8_t* p, int lane) {
-  asm("" : "+s"(p));
-  return ((const __attribute__((address_space(1))) T*)p)[static_cast<uint32_t>(lane)];
-}
-
-__device__ __forceinline__ void store(void* y, int dtype, int64_t i, float v) {
-  if (dtype == MX_BF16) static_cast<bf16_t*>(y)[i] = from_f32<bf16_t>(v);
-  else if (dtype == MX_F16) static_cast<f16_t*>(y)[i] = from_f32<f16_t>(v);
-  else static_cast<float*>(y)[i] = v;
-}
 
 // TX: type of the unquantized tokens, void for codes.
 template <class TX, int SN>
@@ -72,25 +36,10 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
-  // Work: (pass of tokens, SN stripes).  An expert with many tokens has many
-  // passes, each of them workgroups of its own.  Blocks go to the 8 XCDs in turn:
-  // an XCD takes the x-th part of every pass' stripes, or, of many passes, every
-  // eighth one (make_few).
-  const int x = static_cast<int>(blockIdx.x & 7), i = static_cast<int>(blockIdx.x >> 3), d = i / p.part;
-  const int u = p.whole ? d * 8 + x : d, st = (i - d * p.part + (p.whole ? 0 : x * p.part)) * SN;
-  if (u >= p.passes || st * kTileR >= p.n) return;
-  int e = 0, nt = p.tokens;  // without experts there is one pass
-  int64_t row0 = 0, prow = 0;
-  if (p.experts > 0) {
-    const int pass = kFused ? p.per_pass : 32;
-    Segment s;
-    if (!find_segment(p.offsets, p.experts, p.tokens, u, pass, s)) return;
-    const int t0 = __builtin_amdgcn_readfirstlane(s.unit) * pass;
-    e = __builtin_amdgcn_readfirstlane(s.e);
-    nt = min(pass, __builtin_amdgcn_readfirstlane(s.len) - t0);
-    row0 = s.row0 + t0;
-    prow = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(s.prow))) + t0;
-  }
+  FewWork w0;
+  if (!find_pass(p, SN, kFused ? p.per_pass : 32, w0)) return;
+  const int st = w0.st, e = w0.e, nt = w0.nt;
+  const int64_t row0 = w0.row0, prow = w0.prow;
   const int kt = static_cast<int>(p.kt);
   const int64_t stripe = static_cast<int64_t>(e) * p.mat_stripes + st;
   const uint8_t* wsrc = p.w + stripe * p.kt * kTileBytes;
@@ -175,37 +124,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin_few(const FewParams p
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) multiply(q, min(t + q, end - 1), t + q < end);
   }
-  // join the waves' sums in their order, 32 tokens x 32 lines at a time: a
-  // lane holds token l32, lines 8(v/4) + 4 half + v%4
-  float* sums = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int j = 0; j < SN; ++j) {
-    __syncthreads();
-    if (l32 < nt) {
-      float* d = sums + (wave * nt + l32) * kSumStride + 4 * half;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) d[8 * (v / 4) + v % 4] = acc[j][v];
-    }
-    __syncthreads();
-    for (int i = tid; i < nt * 32; i += threads) {
-      const int t = i >> 5, f = i & 31;
-      float s = 0.0f;
-      for (int q = 0; q < waves; ++q) s += sums[(q * nt + t) * kSumStride + f];
-      const int col = (st + j) * 32 + f;
-      if (col < p.n) store(p.y, p.y_dtype, (row0 + t) * p.ldy + col, s);
-    }
-  }
-}
-
-// Stripes of a workgroup: enough workgroups to fill the CUs first, then fewer
-// and longer ones, which share the tokens and the search for the expert.
-int stripes_per_group(int64_t stripes) { return stripes >= 2048 ? 4 : stripes >= 512 ? 2 : 1; }
-
-// Waves of a workgroup: each takes 4 column tiles at least.
-int waves_of(int64_t kt) {
-  int w = kMaxWaves;
-  while (w > 1 && kt < 4 * w) w /= 2;
-  return w;
+  join_sums<SN>(p, acc, reinterpret_cast<float*>(lds), nt, row0, st);
 }
 
 // LDS of a pass: codes and scales of the tokens, and then the waves' sums in
