@@ -77,32 +77,66 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return dpp_max<0x140>(v);
 }
 
-// 8 consecutive elements of a row from column c on; zeros past the row's end.
+// 8 consecutive elements as they are in memory.  Loading them apart from their
+// conversion keeps the loads of many pieces on their way together: a
+// conversion next to its load, in the branch for the row's end, would wait for
+// that load before the next one is issued.
 template <class T>
-__device__ __forceinline__ void load_row8(const T* row, int64_t c, int64_t cols, float* x) {
-  if (c + 8 <= cols) {
-    load8(row + c, x);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
-}
+struct Raw8 { i32x4 v[sizeof(T) / 2]; };
 
-// 8 consecutive elements to column c on of a row of `cols`.
+// ... of a row from column c on; zeros past the row's end.
 template <class T>
-__device__ __forceinline__ void store_row8(T* row, int64_t c, int64_t cols, const float* x) {
+__device__ __forceinline__ Raw8<T> load_raw8(const T* row, int64_t c, int64_t cols) {
+  Raw8<T> r{};
   if (c + 8 <= cols) {
-    struct alignas(16) { T e[8]; } y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y.e[i] = from_f32<T>(x[i]);
-    constexpr int kPieces = 8 * static_cast<int>(sizeof(T)) / 16;
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) r.v[i] = load16(reinterpret_cast<const uint8_t*>(row + c) + 16 * i);
+  } else if (c < cols) {
+    T e[8];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) store16(reinterpret_cast<uint8_t*>(row + c) + 16 * i, reinterpret_cast<const i32x4*>(&y)[i]);
+    for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? row[c + i] : T{};
+    __builtin_memcpy(&r, e, sizeof(r));
+  }
+  return r;
+}
+template <class T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float* x) {
+  T e[8];
+  __builtin_memcpy(e, &r, sizeof(e));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+}
+template <class T>
+__device__ __forceinline__ Raw8<T> pack8(const float* x) {
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(x[i]);
+  Raw8<T> r;
+  __builtin_memcpy(&r, e, sizeof(r));
+  return r;
+}
+template <class T>
+__device__ __forceinline__ void load_row8(const T* row, int64_t c, int64_t cols, float* x) { unpack8(load_raw8(row, c, cols), x); }
+
+// ... to column c on of a row of `cols`.  STREAM: past the caches.
+template <bool STREAM = false, class T>
+__device__ __forceinline__ void store_raw8(T* row, int64_t c, int64_t cols, const Raw8<T>& r) {
+  if (c + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      uint8_t* at = reinterpret_cast<uint8_t*>(row + c) + 16 * i;
+      if constexpr (STREAM) stream16(at, r.v[i]);
+      else store16(at, r.v[i]);
+    }
     return;
   }
+  T e[8];
+  __builtin_memcpy(e, &r, sizeof(e));
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (c + i < cols) row[c + i] = from_f32<T>(x[i]);
+    if (c + i < cols) row[c + i] = e[i];
 }
+template <bool STREAM = false, class T>
+__device__ __forceinline__ void store_row8(T* row, int64_t c, int64_t cols, const float* x) { store_raw8<STREAM>(row, c, cols, pack8<T>(x)); }
 
 }  // namespace mx

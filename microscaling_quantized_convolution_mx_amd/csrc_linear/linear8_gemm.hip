@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(con
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % WM, wn = wave / WM;
   Work w;
-  if (!find_work<TM, TN, CONTRACT>(p, w)) return;
+  if (!find_work<TM, TN, CONTRACT, true>(p, w)) return;
   const int nslices = 2 * w.nsteps;
 
   // Copies of a slice: copy l of wave w takes plane l * kWaves + w of a's tiles,
@@ -273,7 +273,9 @@ Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
     pl.shape = shape;
     pl.tiles_i = (rows + tm - 1) / tm + extra;
     pl.tiles_j = (cols + tn - 1) / tn;
-    pl.units = pl.tiles_i * pl.tiles_j * (op == LIN_WGRAD ? g.ew : 1);
+    // (wgrad with experts: every expert's tiles in eighths, one of each XCD)
+    pl.units = pl.tiles_i * pl.tiles_j;
+    if (op == LIN_WGRAD && g.e > 0) pl.units = (pl.units + 7) / 8 * 8 * g.ew;
     pl.split_steps = static_cast<int>((all_steps + pieces - 1) / pieces);
     pl.splits = pieces > 1 ? static_cast<int>((all_steps + pl.split_steps - 1) / pl.split_steps) : 1;
     const int64_t likely = pl.units - extra * pl.tiles_j / 2;

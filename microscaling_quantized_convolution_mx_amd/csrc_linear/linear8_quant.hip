@@ -76,16 +76,13 @@ __global__ __launch_bounds__(256) void k_lin8_quantize(const Quant8Params p) {
   if (!find_rows(p, by, at)) return;
   const int r0 = 32 * wave + 8 * g;
   const int64_t c = static_cast<int64_t>(bx) * kPad + 8 * q;
+  Raw8<T> raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    raw[i] = load_raw8(static_cast<const T*>(p.src) + (at.row0 + r0 + i) * p.ld, c, r0 + i < at.left ? p.cols : 0);
   float x[8][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r0 + i < at.left && c < p.cols) {
-      load_row8(static_cast<const T*>(p.src) + (at.row0 + r0 + i) * p.ld, c, p.cols, x[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.0f;
-    }
-  }
+  for (int i = 0; i < 8; ++i) unpack8(raw[i], x[i]);
   uint32_t rcode[8], ccode[8];
   if constexpr (SQUARE) {
     uint32_t m = 0;
@@ -163,8 +160,9 @@ __global__ __launch_bounds__(256) void k_lin8_quantize(const Quant8Params p) {
 
 // Workgroups, waves and lanes as in the quantizer, but a wave's rows in the
 // order of memory: a load takes 4 rows that share their lines.  COLS: from the
-// column form, byte by byte through LDS.
-template <class T, bool COLS>
+// column form, byte by byte through LDS.  STREAM: past the caches, rows at
+// multiples of 64 bytes.
+template <class T, bool COLS, bool STREAM>
 __global__ __launch_bounds__(256) void k_lin8_dequantize(const Quant8Params p, T* __restrict__ dst) {
   __shared__ __attribute__((aligned(16))) uint8_t tile[COLS ? kBlockBytes : 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, q = lane & 15;
@@ -216,7 +214,7 @@ __global__ __launch_bounds__(256) void k_lin8_dequantize(const Quant8Params p, T
 #pragma unroll
       for (int j = 0; j < 4; ++j) y[4 * h + j] = v[j] * scale[COLS ? 4 * h + j : 0];
     }
-    store_row8(dst + (at.row0 + r) * p.ld, c, p.cols, y);
+    store_row8<STREAM>(dst + (at.row0 + r) * p.ld, c, p.cols, y);
   }
 }
 
@@ -282,7 +280,12 @@ hipError_t launch_lin8_dequantize(const LinGeom& g, mx_role role, mx_form form, 
   auto as = [&](auto t) {
     using T = decltype(t);
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(n), dim3(256), 0, s, p, static_cast<T*>(dst)); };
-    form == MX_FORM_COLS ? go(k_lin8_dequantize<T, true>) : go(k_lin8_dequantize<T, false>);
+    auto with = [&](auto stream) {
+      constexpr bool S = decltype(stream)::value;
+      form == MX_FORM_COLS ? go(k_lin8_dequantize<T, true, S>) : go(k_lin8_dequantize<T, false, S>);
+    };
+    // (fp32: a lane's 32 bytes are two stores of half lines, which the caches join)
+    sizeof(T) == 2 && lin_dequantize_streams(dst, dtype, ld) ? with(std::true_type{}) : with(std::false_type{});
   };
   switch (dtype) {
     case MX_BF16: as(bf16_t{}); break;

@@ -61,7 +61,10 @@ struct Work {
 // Work: (expert, row tile, column tile, split).  Blocks go to the 8 XCDs in
 // turn; XCD x takes the x-th eighth of the work, so that what its blocks
 // share stays in its L2.  False where the block has none.
-template <int TM, int TN, bool CONTRACT>
+// SPREAD (CONTRACT with experts): XCD x takes the x-th eighth of every expert's
+// tiles instead, so that experts with many tokens are all XCDs' work alike; the
+// grid has room for a multiple of 8 tiles of each.
+template <int TM, int TN, bool CONTRACT, bool SPREAD = false>
 __device__ __forceinline__ bool find_work(const ProductParams& p, Work& o) {
   int ti, tj, sp = 0;
   int64_t arow = 0, brow = 0, orow = 0, rleft, k0 = 0, out = 0;
@@ -75,12 +78,18 @@ __device__ __forceinline__ bool find_work(const ProductParams& p, Work& o) {
       find_segment(p.offsets, p.experts, p.tokens, -1, TM, s, &ti_all);
       total = static_cast<int64_t>(ti_all) * p.tiles_j;
     }
+    const int64_t plane = static_cast<int64_t>(p.tiles_i) * p.tiles_j;
     const int64_t per = (total + 7) / 8;
     const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
     int64_t w = x * per + i;
-    if (i >= per || w >= total) return false;
+    if (SPREAD && CONTRACT && p.experts > 0) {
+      const int64_t part = (plane + 7) / 8, e = i / part, in = x * part + (i - e * part);
+      if (e >= p.experts || in >= plane) return false;
+      w = e * plane + in;
+    } else if (i >= per || w >= total) {
+      return false;
+    }
     // groups of 4 row tiles, walked column by column
-    const int64_t plane = static_cast<int64_t>(p.tiles_i) * p.tiles_j;
     int rows_t = p.tiles_i;
     int z = 0;
     if (CONTRACT || p.experts == 0) {

@@ -47,125 +47,233 @@ __device__ __forceinline__ void store_any(void* p, mx_dtype t, int64_t row, int6
   else store_row8(static_cast<float*>(p) + row, c, cols, x);
 }
 
+// v of another lane of the row of 16 (DPP).
 template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+__device__ __forceinline__ float dpp(float v) { return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true)); }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b), CTRL, 0xF, 0xF, true));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(b >> 32), CTRL, 0xF, 0xF, true));
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-// The sum over a wave, in every lane: rows of 16 lanes, then the four rows.
-__device__ __forceinline__ float wave_sum(float v) {
-  v = dpp_add<0x140>(dpp_add<0x141>(dpp_add<0x4E>(dpp_add<0xB1>(v))));
-  const int b = __float_as_int(v);
-  return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
-         (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+__device__ __forceinline__ float from_lane(float v, int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); }
+__device__ __forceinline__ double from_lane(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b), l));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), l));
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// The sum over a row's TPR threads.  `buf` is used in turn, so that one barrier
-// per row is enough: a wave that writes half `turn` again has passed the
-// barrier of the row between, which all have reached after reading it.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*buf)[TPR / 64], int turn) {
-  v = wave_sum(v);
+// The sum over a wave, in every lane: rows of 16 lanes (pairs, fours, mirrored
+// halves), then the four rows.
+template <class S>
+__device__ __forceinline__ S wave_sum(S v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
+}
+
+// The sums over RB rows' TPR threads.  `buf` is used in turn, so that one
+// barrier is enough: a wave that writes half `turn` again has passed the
+// barrier between, which all have reached after reading it.
+template <int TPR, int RB, class S>
+__device__ __forceinline__ void row_sums(S (&v)[RB], S (*buf)[RB][TPR / 64], int turn) {
+#pragma unroll
+  for (int b = 0; b < RB; ++b) v[b] = wave_sum(v[b]);
   if constexpr (TPR > 64) {
     const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) buf[turn][wave] = v;
-    __syncthreads();
-    v = buf[turn][0];
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v += buf[turn][w];
+      for (int b = 0; b < RB; ++b) buf[turn][b][wave] = v[b];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      v[b] = buf[turn][b][0];
+#pragma unroll
+      for (int w = 1; w < TPR / 64; ++w) v[b] += buf[turn][b][w];
+    }
   }
-  return v;
 }
 
-// 8 values as codes of the 8-bit row form: 16 lanes share a block of 128.
-__device__ __forceinline__ void store_codes(const FwdParams& p, int64_t row, int64_t c, const float* y) {
+// 1 / sqrt(x): the fp32 value and one Newton step in fp64.
+__device__ __forceinline__ double inverse_root(double x) {
+  const float f = 1.0f / __builtin_sqrtf(static_cast<float>(x));
+  const double r = f;
+  return f > 0.0f && f < __builtin_inff() ? r * (1.5 - 0.5 * x * r * r) : r;
+}
+
+// t * (hi + lo) * w, of which hi + lo is rstd, rounded to fp32, inexact results to the neighbour with an
+// odd last bit, so that rounding the result again, to E4M3, gives what rounding
+// the product once would: codes are off only where rstd's own error, some
+// 10^-9, reaches a tie.
+__device__ __forceinline__ float odd_product(float t, float hi, float lo, float w) {
+  const float h = t * hi, e = __builtin_fmaf(t, lo, __builtin_fmaf(t, hi, -h));
+  const float y = h * w;
+  const float d = __builtin_fmaf(h, w, -y) + e * w;  // what the product has more than y
+  // towards zero where the signs differ (d is 0 where y is), and then odd; an
+  // overflow stays as it is, d being Inf then
+  const int b = __float_as_int(y), odd = (b + ((__float_as_int(d) ^ b) >> 31)) | 1;
+  constexpr int kFinite = 0x198;  // a normal or subnormal number of either sign
+  return __int_as_float(__builtin_amdgcn_classf(d, kFinite) ? odd : b);
+}
+
+__device__ __forceinline__ int64_t code_place(const FwdParams& p, int64_t row, int64_t c) {
+  return ((row / kTileR) * p.kt + c / kTileC) * k8TileBytes + (c / 16 % 4) * 512 + (row % 32) * 16;
+}
+// 8 values as codes of the 8-bit row form: 16 lanes share a block of 128, whose
+// scale is stored.
+__device__ __forceinline__ uint2 encode_codes(const FwdParams& p, int64_t row, int64_t c, const float* y) {
   const uint32_t code = block8_code(row16_max(amax8(y)));
-  const uint2 w = encode8x8(y, code);
-  uint8_t* at = p.a.codes + ((row / kTileR) * p.kt + c / kTileC) * k8TileBytes + (c / 16 % 4) * 512 + (row % 32) * 16 + c % 16;
-  *reinterpret_cast<uint2*>(at) = w;
   if (c % kPad == 0)
     p.a.scales[(row / kPad * (p.kt / 2) + c / kPad) * k8ScaleBytes + (row % 32) * 4 + row / 32 % 4] = static_cast<uint8_t>(code);
+  return encode8x8(y, code);
+}
+
+template <class T>
+__device__ __forceinline__ void add_residual(Raw8<T>& v, const Raw8<T>& r, float* t) {
+  float b[8];
+  unpack8(v, t);
+  unpack8(r, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] += b[i];
+  v = pack8<T>(t);
+}
+
+// RB rows at a time: their loads are on their way together, and (CODES) the
+// four rows' codes of 16 columns, 64 consecutive bytes, are written together:
+// a wave brings its lanes' halves of 16 bytes and rows in the order of memory
+// through LDS of its own.
+template <class T, int TPR, int CH, int RB, bool CODES>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdParams p) {
+  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;  // groups of rows of a workgroup
+  constexpr int kThreads = TPR * RPW;
+  __shared__ double buf[2][RB][TPR / 64];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[CODES && RB > 1 ? kThreads / 64 : 1][RB * 512];
+  const int t = threadIdx.x % TPR, lane = threadIdx.x & 63;
+  float w[CH][8];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) load_any(p.a.weight, p.a.w_dtype, 0, (j * TPR + t) * 8, p.features, w[j]);
+  const int rows = CODES ? p.padded_rows : p.tokens;
+  int turn = 0;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR) * RB; row < rows;
+       row += static_cast<int64_t>(gridDim.x) * RPW * RB, turn ^= 1) {
+    Raw8<T> v[RB][CH];
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        v[b][j] = load_raw8(static_cast<const T*>(p.a.x) + (row + b) * p.a.ldx, (j * TPR + t) * 8, row + b < p.tokens ? p.features : 0);
+    double s[RB];
+    if (p.a.residual) {
+      Raw8<T> r[RB][CH];
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+          r[b][j] = load_raw8(static_cast<const T*>(p.a.residual) + (row + b) * p.a.ldr, (j * TPR + t) * 8, row + b < p.tokens ? p.features : 0);
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          float sum[8];
+          add_residual(v[b][j], r[b][j], sum);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      float q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        float x[8];
+        unpack8(v[b][j], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q += x[i] * x[i];
+      }
+      s[b] = q;
+    }
+    row_sums<TPR, RB>(s, buf, turn);
+    float hi[RB], lo[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const double r = inverse_root(s[b] / p.features + static_cast<double>(p.eps));
+      hi[b] = static_cast<float>(r);
+      lo[b] = static_cast<float>(r - hi[b]);
+      if (p.a.rstd && t == 0 && row + b < p.tokens) p.a.rstd[row + b] = hi[b];
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * TPR + t) * 8;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const bool in = row + b < p.tokens && c < p.features;
+        if (in && p.a.total) store_raw8(static_cast<T*>(p.a.total) + (row + b) * p.a.ldt, c, p.features, v[b][j]);
+        float x[8], y[8];
+        unpack8(v[b][j], x);
+        if (in && p.a.y) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = x[i] * hi[b] * w[j][i];
+          store_any(p.a.y, p.a.y_dtype, (row + b) * p.a.ldy, c, p.features, y);
+        }
+        if constexpr (CODES) {
+          if (c < 8 * p.chunks) {
+            // (a row's padded columns are zeros of x and the weight; where rstd is not finite they share a block of NaNs)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = row + b < p.tokens ? odd_product(x[i], hi[b], lo[b], w[j][i]) : 0.0f;
+            const uint2 e = encode_codes(p, row + b, c, y);
+            if constexpr (RB == 1) *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = e;
+            else *reinterpret_cast<uint2*>(stage[threadIdx.x >> 6] + ((lane / 2) * RB + b) * 16 + 8 * (lane % 2)) = e;
+          }
+        }
+      }
+      if constexpr (CODES && RB > 1) {
+        __builtin_amdgcn_wave_barrier();
+        const int c0 = c - 8 * lane;  // the wave's first column
+#pragma unroll
+        for (int k = 0; k < (RB + 1) / 2; ++k) {
+          const int piece = k * 64 + lane, cp = c0 + piece / RB * 16;
+          if (cp < 8 * p.chunks)
+            *reinterpret_cast<i32x4*>(p.a.codes + code_place(p, row + piece % RB, cp)) = *reinterpret_cast<const i32x4*>(stage[threadIdx.x >> 6] + piece * 16);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
 }
 
 template <class T>
 __device__ __forceinline__ void load_total(const FwdParams& p, int64_t row, int64_t c, float* v) {
-  load_row8(static_cast<const T*>(p.a.x) + row * p.a.ldx, c, p.features, v);
-  if (p.a.residual) {
-    float r[8];
-    load_row8(static_cast<const T*>(p.a.residual) + row * p.a.ldr, c, p.features, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(from_f32<T>(v[i] + r[i]));
-  }
-}
-
-template <class T, int TPR, int CH, bool CODES>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdParams p) {
-  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;  // rows of a workgroup
-  __shared__ float buf[2][TPR / 64];
-  const int t = threadIdx.x % TPR;
-  float w[CH][8];
-#pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    const int c = (j * TPR + t) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[j][i] = 0.0f;
-    if (c < p.features) load_any(p.a.weight, p.a.w_dtype, 0, c, p.features, w[j]);
-  }
-  const int rows = CODES ? p.padded_rows : p.tokens;
-  int turn = 0;
-  for (int row = blockIdx.x * RPW + threadIdx.x / TPR; row < rows; row += gridDim.x * RPW, turn ^= 1) {
-    float v[CH][8];
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (row < p.tokens && c < p.features) load_total<T>(p, row, c, v[j]);
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < CH; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[j][i] * v[j][i];
-    s = row_sum<TPR>(s, buf, turn);
-    const float r = 1.0f / __builtin_sqrtf(s / static_cast<float>(p.features) + p.eps);
-    if (p.a.rstd && t == 0 && row < p.tokens) p.a.rstd[row] = r;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
-      const bool in = row < p.tokens && c < p.features;
-      if (in && p.a.total) store_row8(static_cast<T*>(p.a.total) + row * p.a.ldt, c, p.features, v[j]);
-      float y[8];
-      // (padding is zero also where rstd is not finite)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = in && c + i < p.features ? v[j][i] * r * w[j][i] : 0.0f;
-      if (in && p.a.y) store_any(p.a.y, p.a.y_dtype, row * p.a.ldy, c, p.features, y);
-      if constexpr (CODES) {
-        if (c < 8 * p.chunks) store_codes(p, row, c, y);
-      }
-    }
-  }
+  Raw8<T> x = load_raw8(static_cast<const T*>(p.a.x) + row * p.a.ldx, c, p.features);
+  if (p.a.residual) add_residual(x, load_raw8(static_cast<const T*>(p.a.residual) + row * p.a.ldr, c, p.features), v);
+  unpack8(x, v);
 }
 
 // Rows of any length, read twice.
 template <class T, bool CODES>
 __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
   constexpr int TPR = 1024;
-  __shared__ float buf[2][TPR / 64];
+  __shared__ double buf[2][1][TPR / 64];
   const int rows = CODES ? p.padded_rows : p.tokens;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-    float s = 0.0f;
+    double s[1] = {0.0};
     if (row < p.tokens) {
+      float q = 0.0f;
       for (int64_t c = 8 * threadIdx.x; c < p.features; c += 8 * TPR) {
         float v[8];
         load_total<T>(p, row, c, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+        for (int i = 0; i < 8; ++i) q += v[i] * v[i];
       }
+      s[0] = q;
     }
-    s = row_sum<TPR>(s, buf, turn);
-    const float r = 1.0f / __builtin_sqrtf(s / static_cast<float>(p.features) + p.eps);
-    if (p.a.rstd && threadIdx.x == 0 && row < p.tokens) p.a.rstd[row] = r;
+    row_sums<TPR, 1>(s, buf, turn);
+    const double r = inverse_root(s[0] / p.features + static_cast<double>(p.eps));
+    const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
+    if (p.a.rstd && threadIdx.x == 0 && row < p.tokens) p.a.rstd[row] = hi;
     for (int64_t c = 8 * threadIdx.x; c < 8 * static_cast<int64_t>(p.chunks); c += 8 * TPR) {
       float v[8] = {}, w[8] = {}, y[8];
       const bool in = row < p.tokens && c < p.features;
@@ -174,65 +282,96 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
         load_any(p.a.weight, p.a.w_dtype, 0, c, p.features, w);
         if (p.a.total) store_row8(static_cast<T*>(p.a.total) + row * p.a.ldt, c, p.features, v);
       }
+      if (in && p.a.y) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = in && c + i < p.features ? v[i] * r * w[i] : 0.0f;
-      if (in && p.a.y) store_any(p.a.y, p.a.y_dtype, row * p.a.ldy, c, p.features, y);
-      if constexpr (CODES) store_codes(p, row, c, y);
+        for (int i = 0; i < 8; ++i) y[i] = v[i] * hi * w[i];
+        store_any(p.a.y, p.a.y_dtype, row * p.a.ldy, c, p.features, y);
+      }
+      if constexpr (CODES) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = in && c + i < p.features ? odd_product(v[i], hi, lo, w[i]) : 0.0f;
+        *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = encode_codes(p, row, c, y);
+      }
     }
   }
 }
 
-template <class T, int TPR, int CH>
+// RB rows at a time, whose loads are on their way together.  SAME: dy has
+// total's type.
+template <class T, bool SAME, int TPR, int CH, int RB>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdParams p) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float buf[2][TPR / 64];
+  __shared__ float buf[2][RB][TPR / 64];
   const int t = threadIdx.x % TPR;
   float w[CH][8], dw[CH][8];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    const int c = (j * TPR + t) * 8;
+    load_any(p.a.weight, p.a.w_dtype, 0, (j * TPR + t) * 8, p.features, w[j]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[j][i] = dw[j][i] = 0.0f;
-    if (c < p.features) load_any(p.a.weight, p.a.w_dtype, 0, c, p.features, w[j]);
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR; row < p.tokens; row += gridDim.x * RPW, turn ^= 1) {
-    const float r = p.a.rstd[row];
-    float g[CH][8], h[CH][8];
-    float s = 0.0f;
+  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR) * RB; row < p.tokens;
+       row += static_cast<int64_t>(gridDim.x) * RPW * RB, turn ^= 1) {
+    Raw8<T> gr[RB][CH], hr[RB][CH], dr[RB][CH];
+    float r[RB], s[RB];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
+    for (int b = 0; b < RB; ++b) {
+      const int cols = row + b < p.tokens ? p.features : 0;
+      r[b] = row + b < p.tokens ? p.a.rstd[row + b] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[j][i] = h[j][i] = 0.0f;
-      if (c < p.features) {
-        load_any(p.a.dy, p.a.dy_dtype, row * p.a.lddy, c, p.features, g[j]);
-        load_row8(static_cast<const T*>(p.a.total) + row * p.a.ldt, c, p.features, h[j]);
+      for (int j = 0; j < CH; ++j) {
+        const int c = (j * TPR + t) * 8;
+        if constexpr (SAME) gr[b][j] = load_raw8(static_cast<const T*>(p.a.dy) + (row + b) * p.a.lddy, c, cols);
+        hr[b][j] = load_raw8(static_cast<const T*>(p.a.total) + (row + b) * p.a.ldt, c, cols);
+        dr[b][j] = {};
+        if (p.a.dtotal) dr[b][j] = load_raw8(static_cast<const T*>(p.a.dtotal) + (row + b) * p.a.lddt, c, cols);
       }
+    }
+    // dy, h and the sum of g h; g and h are computed again below, which takes fewer registers than keeping them
+    auto terms = [&](int b, int j, float* dy, float* h) {
+      const int c = (j * TPR + t) * 8;
+      if constexpr (SAME) unpack8(gr[b][j], dy);
+      else load_any(p.a.dy, p.a.dy_dtype, (row + b) * p.a.lddy, c, row + b < p.tokens ? p.features : 0, dy);
+      unpack8(hr[b][j], h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[j][i] *= r;
-        dw[j][i] += g[j][i] * h[j][i];
-        g[j][i] *= w[j][i];
-        s += g[j][i] * h[j][i];
+      for (int i = 0; i < 8; ++i) h[i] *= r[b];
+    };
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      s[b] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        float dy[8], h[8];
+        terms(b, j, dy, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw[j][i] += dy[i] * h[i];
+          s[b] += (dy[i] * w[j][i]) * h[i];
+        }
       }
     }
     if (!p.a.dx) continue;
-    const float m = row_sum<TPR>(s, buf, turn) / static_cast<float>(p.features);
+    row_sums<TPR, RB>(s, buf, turn);
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
-      if (c >= p.features) continue;
-      float d[8] = {};
-      if (p.a.dtotal) load_row8(static_cast<const T*>(p.a.dtotal) + row * p.a.lddt, c, p.features, d);
+    for (int b = 0; b < RB; ++b) {
+      if (row + b >= p.tokens) break;
+      const float m = s[b] / static_cast<float>(p.features);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] += r * (g[j][i] - h[j][i] * m);
-      store_row8(static_cast<T*>(p.a.dx) + row * p.a.lddx, c, p.features, d);
+      for (int j = 0; j < CH; ++j) {
+        const int c = (j * TPR + t) * 8;
+        float dy[8], h[8], d[8];
+        terms(b, j, dy, h);
+        unpack8(dr[b][j], d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] += r[b] * (dy[i] * w[j][i] - h[i] * m);
+        if (c < p.features) store_row8(static_cast<T*>(p.a.dx) + (row + b) * p.a.lddx, c, p.features, d);
+      }
     }
   }
   if (!p.partial) return;
   if constexpr (RPW > 1) {
-    // the rows' waves in their order
+    // the workgroup's waves in their order
     __shared__ float sum[RPW][TPR * 8 + 8];
     const int rw = threadIdx.x / TPR;
 #pragma unroll
@@ -259,13 +398,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdPar
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
   constexpr int TPR = 1024;
-  __shared__ float buf[2][TPR / 64];
+  __shared__ float buf[2][1][TPR / 64];
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.tokens; row += gridDim.x, turn ^= 1) {
     const float r = p.a.rstd[row];
     float m = 0.0f;
     for (int pass = 0; pass < 2; ++pass) {
-      float s = 0.0f;
+      float s[1] = {0.0f};
       for (int64_t c = 8 * threadIdx.x; c < p.features; c += 8 * TPR) {
         float g[8], h[8], w[8];
         load_any(p.a.dy, p.a.dy_dtype, row * p.a.lddy, c, p.features, g);
@@ -275,7 +414,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
         for (int i = 0; i < 8; ++i) {
           h[i] *= r;
           g[i] *= w[i];
-          s += g[i] * h[i];
+          s[0] += g[i] * h[i];
         }
         if (pass == 0) continue;
         float d[8] = {};
@@ -284,7 +423,10 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
         for (int i = 0; i < 8; ++i) d[i] += r * (g[i] - h[i] * m);
         store_row8(static_cast<T*>(p.a.dx) + row * p.a.lddx, c, p.features, d);
       }
-      if (pass == 0) m = row_sum<TPR>(s, buf, turn) / static_cast<float>(p.features);
+      if (pass == 0) {
+        row_sums<TPR, 1>(s, buf, turn);
+        m = s[0] / static_cast<float>(p.features);
+      }
     }
   }
 }
@@ -326,20 +468,20 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ 
   }
 }
 
-// Threads of a row of `chunks` pieces, which they hold in registers (1 or 2
-// each, or 4 of 256 threads), or 0 where that is too much.
-int threads_per_row(int64_t chunks) { return chunks <= 128 ? 64 : chunks <= 1024 ? 256 : chunks <= 2048 ? 1024 : 0; }
-int rows_per_group(int tpr) { return tpr == 64 ? 4 : 1; }
+// Threads of a row of `chunks` pieces, which they hold in registers, 1 or 2 each,
+// or 0 where those are too few.
+int threads_per_row(int64_t chunks) { return chunks <= 128 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? 512 : chunks <= 2048 ? 1024 : 0; }
 
-// Workgroups: enough for all CUs to be full, then each takes more rows.
-int fwd_groups(int64_t rows, int tpr) {
-  const int64_t n = (rows + rows_per_group(tpr) - 1) / rows_per_group(tpr);
-  return static_cast<int>(std::min<int64_t>(n, tpr == 1024 ? 512 : 2048));
-}
-// (of whose partial sums of the weight's gradient all are read again)
-int bwd_groups(int64_t rows, int tpr) {
-  const int64_t n = (rows + rows_per_group(tpr) - 1) / rows_per_group(tpr);
-  return static_cast<int>(std::min<int64_t>(n, 512));
+// Rows that a thread has in registers at a time: one of few rows, so that they
+// are spread over the CUs, and one where 1024 threads leave it 128 registers.
+constexpr int kManyRows = 1024;
+constexpr int rows_at_once(int tpr, bool bwd) { return tpr == 1024 ? 1 : bwd ? 2 : 4; }
+
+// Workgroups: enough for all CUs to be full, then each takes more rows.  (Of the
+// backward pass all read partial sums of the weight's gradient are read again.)
+int norm_groups(int64_t rows, int tpr, int at_once, bool bwd) {
+  const int64_t per = (tpr == 64 ? 4 : 1) * at_once, n = (rows + per - 1) / per;
+  return static_cast<int>(std::min<int64_t>(n, bwd || tpr == 1024 ? 512 : 2048));
 }
 
 // go(threads per row, pieces of a thread) as compile-time constants
@@ -347,13 +489,12 @@ template <class F>
 void by_size(int64_t chunks, F&& go) {
   const int tpr = threads_per_row(chunks);
   auto with = [&](auto t) {
-    const int64_t n = (chunks + decltype(t)::value - 1) / decltype(t)::value;
-    if (n <= 1) go(t, std::integral_constant<int, 1>{});
-    else if (n <= 2) go(t, std::integral_constant<int, 2>{});
-    else if constexpr (decltype(t)::value == 256) go(t, std::integral_constant<int, 4>{});
+    if (chunks <= decltype(t)::value) go(t, std::integral_constant<int, 1>{});
+    else go(t, std::integral_constant<int, 2>{});
   };
   if (tpr == 64) with(std::integral_constant<int, 64>{});
   else if (tpr == 256) with(std::integral_constant<int, 256>{});
+  else if (tpr == 512) with(std::integral_constant<int, 512>{});
   else with(std::integral_constant<int, 1024>{});
 }
 
@@ -378,22 +519,32 @@ hipError_t launch_norm_fwd(const mx_norm_desc& d, const NormFwd& a, hipStream_t 
   p.chunks = static_cast<int>(codes ? pad128(d.features) / 8 : (static_cast<int64_t>(d.features) + 7) / 8);
   const int64_t rows = codes ? p.padded_rows : p.tokens;
   if (rows == 0) return hipSuccess;
-  const int tpr = threads_per_row(p.chunks);
   by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    auto go = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, dim3(fwd_groups(rows, tpr ? tpr : 1024)), dim3(threads), 0, s, p); };
-    if (tpr == 0) codes ? go(k_norm_fwd_long<T, true>, 1024) : go(k_norm_fwd_long<T, false>, 1024);
-    else by_size(p.chunks, [&](auto n, auto ch) {
-      constexpr int N = decltype(n)::value, C = decltype(ch)::value;
-      codes ? go(k_norm_fwd<T, N, C, true>, N < 256 ? 256 : N) : go(k_norm_fwd<T, N, C, false>, N < 256 ? 256 : N);
+    if (threads_per_row(p.chunks) == 0) {
+      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(norm_groups(rows, 1024, 1, false)), dim3(1024), 0, s, p); };
+      codes ? go(k_norm_fwd_long<T, true>) : go(k_norm_fwd_long<T, false>);
+    } else by_size(p.chunks, [&](auto n, auto ch) {
+      constexpr int N = decltype(n)::value, C = decltype(ch)::value, R = rows_at_once(N, false);
+      auto go = [&](auto kern, int at_once) { hipLaunchKernelGGL(kern, dim3(norm_groups(rows, N, at_once, false)), dim3(N < 256 ? 256 : N), 0, s, p); };
+      if (d.tokens >= kManyRows) codes ? go(k_norm_fwd<T, N, C, R, true>, R) : go(k_norm_fwd<T, N, C, R, false>, R);
+      else codes ? go(k_norm_fwd<T, N, C, 1, true>, 1) : go(k_norm_fwd<T, N, C, 1, false>, 1);
     });
   });
   return hipGetLastError();
 }
 
-size_t norm_workspace(const mx_norm_desc& d) {
+namespace {
+// Workgroups of the backward pass, whose partial sums the workspace holds: no
+// more than with one row at a time.
+int bwd_groups(const mx_norm_desc& d) {
   const int tpr = threads_per_row((static_cast<int64_t>(d.features) + 7) / 8);
-  return d.tokens == 0 ? 0 : sizeof(float) * static_cast<size_t>(bwd_groups(d.tokens, tpr ? tpr : 1024)) * static_cast<size_t>(d.features);
+  return norm_groups(d.tokens, tpr ? tpr : 1024, 1, true);
+}
+}  // namespace
+
+size_t norm_workspace(const mx_norm_desc& d) {
+  return d.tokens == 0 ? 0 : sizeof(float) * static_cast<size_t>(bwd_groups(d)) * static_cast<size_t>(d.features);
 }
 
 hipError_t launch_norm_bwd(const mx_norm_desc& d, const NormBwd& a, void* workspace, hipStream_t s) {
@@ -403,16 +554,22 @@ hipError_t launch_norm_bwd(const mx_norm_desc& d, const NormBwd& a, void* worksp
   p.features = d.features;
   p.partial = a.dweight && d.tokens > 0 ? static_cast<float*>(workspace) : nullptr;
   const int64_t chunks = (static_cast<int64_t>(d.features) + 7) / 8;
-  const int tpr = threads_per_row(chunks), groups = bwd_groups(d.tokens, tpr ? tpr : 1024);
+  int groups = bwd_groups(d);
   if (d.tokens > 0) by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    if (tpr == 0) {
+    if (threads_per_row(chunks) == 0) {
       // (first, since dx may be in dy's place)
       if (p.partial) hipLaunchKernelGGL(k_norm_dweight<T>, dim3(static_cast<unsigned>((chunks + 255) / 256), groups), dim3(256), 0, s, p);
       if (a.dx) hipLaunchKernelGGL(k_norm_bwd_long<T>, dim3(groups), dim3(1024), 0, s, p);
     } else by_size(chunks, [&](auto n, auto ch) {
-      constexpr int N = decltype(n)::value, C = decltype(ch)::value;
-      hipLaunchKernelGGL((k_norm_bwd<T, N, C>), dim3(groups), dim3(N < 256 ? 256 : N), 0, s, p);
+      constexpr int N = decltype(n)::value, C = decltype(ch)::value, R = rows_at_once(N, true);
+      auto go = [&](auto kern, int at_once) {
+        groups = norm_groups(d.tokens, N, at_once, true);
+        hipLaunchKernelGGL(kern, dim3(groups), dim3(N < 256 ? 256 : N), 0, s, p);
+      };
+      if (a.dy_dtype != a.dtype) go(k_norm_bwd<T, false, N, C, 1>, 1);
+      else if (d.tokens >= kManyRows) go(k_norm_bwd<T, true, N, C, R>, R);
+      else go(k_norm_bwd<T, true, N, C, 1>, 1);
     });
   });
   if (a.dweight)

@@ -200,6 +200,8 @@ __global__ __launch_bounds__(256) void k_route_gather(const MoveParams p) {
   }
 }
 
+constexpr int kLoads = 4;  // choices whose loads are on their way together
+
 template <class T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_route_combine(const MoveParams p) {
   const int per = 256 >> p.lanes, l = threadIdx.x & ((1 << p.lanes) - 1);
@@ -208,21 +210,32 @@ __global__ __launch_bounds__(256) void k_route_combine(const MoveParams p) {
     const float* weight = WEIGHTED ? p.weight + t * p.choices : nullptr;
     for (int64_t c = static_cast<int64_t>(l) * 8; c < p.features; c += 8 << p.lanes) {
       float s[8] = {};
-      for (int j = 0; j < p.choices; ++j) {
-        const int r = rows[j];
-        if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(p.limit)) continue;
-        float v[8];
-        load_row8(static_cast<const T*>(p.a) + r * p.lda, c, p.features, v);
-        const float w = WEIGHTED ? weight[j] : 1.0f;
+      for (int j0 = 0; j0 < p.choices; j0 += kLoads) {
+        Raw8<T> raw[kLoads];
+        bool has[kLoads];
+        float w[kLoads];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += WEIGHTED ? w * v[i] : v[i];
+        for (int j = 0; j < kLoads; ++j) {
+          const int q = min(j0 + j, p.choices - 1), r = rows[q];
+          has[j] = j0 + j < p.choices && static_cast<uint32_t>(r) < static_cast<uint32_t>(p.limit);
+          raw[j] = load_raw8(static_cast<const T*>(p.a) + (has[j] ? r : 0) * p.lda, c, has[j] ? p.features : 0);
+          w[j] = WEIGHTED ? weight[q] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          float v[8];
+          unpack8(raw[j], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (has[j]) s[i] += WEIGHTED ? w[j] * v[i] : v[i];
+        }
       }
       store_row8(static_cast<T*>(p.out) + t * p.ldo, c, p.features, s);
     }
   }
 }
 
-constexpr int kAtOnce = 8;  // choices whose sums a lane holds
+constexpr int kAtOnce = 4;  // choices whose rows are read, and sums held, together
 
 template <class T>
 __global__ __launch_bounds__(256) void k_route_combine_bwd(const MoveParams p) {
@@ -241,14 +254,21 @@ __global__ __launch_bounds__(256) void k_route_combine_bwd(const MoveParams p) {
         s[j] = 0.0f;
       }
       for (int64_t c = static_cast<int64_t>(l) * 8; c < p.features; c += 8 << p.lanes) {
+        const Raw8<T> graw = load_raw8(dout, c, p.features);
+        Raw8<T> yraw[kAtOnce];
+        if (p.dweight) {
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            if (j0 + j < p.choices) yraw[j] = load_raw8(static_cast<const T*>(p.y) + max(r[j], 0) * p.ldy, c, r[j] < 0 ? 0 : p.features);
+        }
         float g[8];
-        load_row8(dout, c, p.features, g);
+        unpack8(graw, g);
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
           if (r[j] < 0) continue;
           if (p.dweight) {
             float v[8];
-            load_row8(static_cast<const T*>(p.y) + r[j] * p.ldy, c, p.features, v);
+            unpack8(yraw[j], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[j] += g[i] * v[i];
           }

@@ -86,6 +86,17 @@ def _like(t, shape, dt: int, other: str, what: str):
     return p, ld, at
 
 
+def _q(q, d):
+    """(mx_linear_qtensor, device) of a tensor whose row form takes the norm in 8 bits."""
+    if isinstance(q, _l8.Linear8QTensor):
+        padded = (d.tokens + 127) // 128 * ((d.features + 127) // 128)  # blocks of 128x128
+        have = q.bytes.get(_l.MX_FORM_ROWS)
+        if have is not None and q.is_cuda and have[0] >= 16384 * padded and have[1] >= 128 * padded:
+            return q.c, q.device_index
+    # what has no room, or is something else, is told apart as the 8-bit layers do
+    return _l8._q(q, _l.mx_linear_desc(d.tokens, 1, d.features, 0, 1), _mx.MX_ROLE_ACT, (_l.MX_FORM_ROWS,), "yq")
+
+
 def mx_norm_fwd(d: mx_norm_desc, x, weight, y=None, residual=None, total=None, yq=None, rstd=None, stream=None) -> None:
     """total = x + residual; y = total * rstd * weight, also or instead in 8 bits (yq, a Linear8QTensor of the
     activation that the next layer takes)."""
@@ -98,7 +109,7 @@ def mx_norm_fwd(d: mx_norm_desc, x, weight, y=None, residual=None, total=None, y
     py, ydt, ldy, yat = _l._matrix(y, shape, "y")
     q = qat = None
     if yq is not None:
-        q, qat = _l8._q(yq, _l.mx_linear_desc(d.tokens, 1, d.features, 0, 1), _mx.MX_ROLE_ACT, (_l.MX_FORM_ROWS,), "yq")
+        q, qat = _q(yq, d)
     ps, sat = _f32(rstd, d.tokens, "rstd")
     _l._check(L.mx_norm_fwd(d, px, ldx, pr, ldr, dt, pw, wdt, pt, ldt, py, ydt, ldy, q, ps,
                             _mx._stream(stream, xat, rat, wat, tat, yat, qat, sat)), "mx_norm_fwd")
