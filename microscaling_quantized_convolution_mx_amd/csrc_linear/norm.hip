@@ -76,27 +76,21 @@ __device__ __forceinline__ S wave_sum(S v) {
   return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 
-// The sums over RB rows' TPR threads.  `buf` is used in turn, so that one
-// barrier is enough: a wave that writes half `turn` again has passed the
-// barrier between, which all have reached after reading it.
-template <int TPR, int RB, class S>
-__device__ __forceinline__ void row_sums(S (&v)[RB], S (*buf)[RB][TPR / 64], int turn) {
-#pragma unroll
-  for (int b = 0; b < RB; ++b) v[b] = wave_sum(v[b]);
-  if constexpr (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int b = 0; b < RB; ++b) buf[turn][b][wave] = v[b];
-    }
+// The sum over a row, a wave's (WAVE) or the workgroup's of at most MOST threads.
+// `buf` is used in turn, so that one barrier is enough: a wave that writes half
+// `turn` again has passed the barrier between, which all have reached after
+// reading it.
+template <bool WAVE, int MOST, class S>
+__device__ __forceinline__ S row_sum(S v, S (*buf)[MOST / 64], int turn) {
+  v = wave_sum(v);
+  if constexpr (!WAVE) {
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) buf[turn][wave] = v;
     __syncthreads();
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      v[b] = buf[turn][b][0];
-#pragma unroll
-      for (int w = 1; w < TPR / 64; ++w) v[b] += buf[turn][b][w];
-    }
+    v = buf[turn][0];
+    for (int w = 1; w < waves; ++w) v += buf[turn][w];
   }
+  return v;
 }
 
 // 1 / sqrt(x): the fp32 value and one Newton step in fp64.
@@ -143,103 +137,89 @@ __device__ __forceinline__ void add_residual(Raw8<T>& v, const Raw8<T>& r, float
   v = pack8<T>(t);
 }
 
-// RB rows at a time: their loads are on their way together, and (CODES) the
-// four rows' codes of 16 columns, 64 consecutive bytes, are written together:
-// a wave brings its lanes' halves of 16 bytes and rows in the order of memory
-// through LDS of its own.
-template <class T, int TPR, int CH, int RB, bool CODES>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdParams p) {
-  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;  // groups of rows of a workgroup
-  constexpr int kThreads = TPR * RPW;
-  __shared__ double buf[2][RB][TPR / 64];
-  __shared__ __attribute__((aligned(16))) uint8_t stage[CODES && RB > 1 ? kThreads / 64 : 1][RB * 512];
-  const int t = threadIdx.x % TPR, lane = threadIdx.x & 63;
+// Rows are taken GROUP at a time, one after the other.  With GROUP = 4 the codes
+// of 4 rows are written together, 64 consecutive bytes of 16 columns each: a
+// wave keeps its columns' codes in LDS of its own until it has all four.
+template <class T, bool WAVE, int MOST, int CH, bool CODES, int GROUP>
+__global__ __launch_bounds__(MOST) void k_norm_fwd(const FwdParams p) {
+  const int tpr = WAVE ? 64 : blockDim.x;     // threads of a row
+  constexpr int RPW = WAVE ? MOST / 64 : 1;  // rows of a workgroup at a time
+  __shared__ double buf[2][MOST / 64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t stage[];  // GROUP > 1: 512 * GROUP bytes of each wave and piece
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = WAVE ? lane : threadIdx.x;
   float w[CH][8];
 #pragma unroll
-  for (int j = 0; j < CH; ++j) load_any(p.a.weight, p.a.w_dtype, 0, (j * TPR + t) * 8, p.features, w[j]);
+  for (int j = 0; j < CH; ++j) load_any(p.a.weight, p.a.w_dtype, 0, (j * tpr + t) * 8, p.features, w[j]);
   const int rows = CODES ? p.padded_rows : p.tokens;
   int turn = 0;
-  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR) * RB; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * RPW * RB, turn ^= 1) {
-    Raw8<T> v[RB][CH];
+  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * RPW + (WAVE ? wave : 0)) * GROUP; row0 < rows;
+       row0 += static_cast<int64_t>(gridDim.x) * RPW * GROUP) {
+    for (int b = 0; b < GROUP; ++b, turn ^= 1) {
+      const int64_t row = row0 + b;
+      const bool in = row < p.tokens;
+      Raw8<T> v[CH];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-        v[b][j] = load_raw8(static_cast<const T*>(p.a.x) + (row + b) * p.a.ldx, (j * TPR + t) * 8, row + b < p.tokens ? p.features : 0);
-    double s[RB];
-    if (p.a.residual) {
-      Raw8<T> r[RB][CH];
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
+      for (int j = 0; j < CH; ++j) v[j] = load_raw8(static_cast<const T*>(p.a.x) + row * p.a.ldx, (j * tpr + t) * 8, in ? p.features : 0);
+      if (p.a.residual) {
+        Raw8<T> r[CH];
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-          r[b][j] = load_raw8(static_cast<const T*>(p.a.residual) + (row + b) * p.a.ldr, (j * TPR + t) * 8, row + b < p.tokens ? p.features : 0);
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
+          r[j] = load_raw8(static_cast<const T*>(p.a.residual) + row * p.a.ldr, (j * tpr + t) * 8, in ? p.features : 0);
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
           float sum[8];
-          add_residual(v[b][j], r[b][j], sum);
+          add_residual(v[j], r[j], sum);
         }
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
+      }
       float q = 0.0f;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         float x[8];
-        unpack8(v[b][j], x);
+        unpack8(v[j], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) q += x[i] * x[i];
       }
-      s[b] = q;
-    }
-    row_sums<TPR, RB>(s, buf, turn);
-    float hi[RB], lo[RB];
+      const double s = row_sum<WAVE, MOST>(static_cast<double>(q), buf, turn);
+      const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
+      const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
+      if (p.a.rstd && t == 0 && in) p.a.rstd[row] = hi;
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const double r = inverse_root(s[b] / p.features + static_cast<double>(p.eps));
-      hi[b] = static_cast<float>(r);
-      lo[b] = static_cast<float>(r - hi[b]);
-      if (p.a.rstd && t == 0 && row + b < p.tokens) p.a.rstd[row + b] = hi[b];
-    }
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = (j * TPR + t) * 8;
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const bool in = row + b < p.tokens && c < p.features;
-        if (in && p.a.total) store_raw8(static_cast<T*>(p.a.total) + (row + b) * p.a.ldt, c, p.features, v[b][j]);
+      for (int j = 0; j < CH; ++j) {
+        const int c = (j * tpr + t) * 8;
         float x[8], y[8];
-        unpack8(v[b][j], x);
-        if (in && p.a.y) {
+        unpack8(v[j], x);
+        if (in && c < p.features) {
+          if (p.a.total) store_raw8(static_cast<T*>(p.a.total) + row * p.a.ldt, c, p.features, v[j]);
+          if (p.a.y) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i] * hi[b] * w[j][i];
-          store_any(p.a.y, p.a.y_dtype, (row + b) * p.a.ldy, c, p.features, y);
+            for (int i = 0; i < 8; ++i) y[i] = x[i] * hi * w[j][i];
+            store_any(p.a.y, p.a.y_dtype, row * p.a.ldy, c, p.features, y);
+          }
         }
         if constexpr (CODES) {
           if (c < 8 * p.chunks) {
             // (a row's padded columns are zeros of x and the weight; where rstd is not finite they share a block of NaNs)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = row + b < p.tokens ? odd_product(x[i], hi[b], lo[b], w[j][i]) : 0.0f;
-            const uint2 e = encode_codes(p, row + b, c, y);
-            if constexpr (RB == 1) *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = e;
-            else *reinterpret_cast<uint2*>(stage[threadIdx.x >> 6] + ((lane / 2) * RB + b) * 16 + 8 * (lane % 2)) = e;
+            for (int i = 0; i < 8; ++i) y[i] = in ? odd_product(x[i], hi, lo, w[j][i]) : 0.0f;
+            const uint2 e = encode_codes(p, row, c, y);
+            if constexpr (GROUP == 1) *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = e;
+            else *reinterpret_cast<uint2*>(stage + (wave * CH + j) * 512 * GROUP + ((lane / 2) * GROUP + b) * 16 + 8 * (lane % 2)) = e;
           }
         }
       }
-      if constexpr (CODES && RB > 1) {
-        __builtin_amdgcn_wave_barrier();
-        const int c0 = c - 8 * lane;  // the wave's first column
+    }
+    if constexpr (CODES && GROUP > 1) {
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int k = 0; k < (RB + 1) / 2; ++k) {
-          const int piece = k * 64 + lane, cp = c0 + piece / RB * 16;
-          if (cp < 8 * p.chunks)
-            *reinterpret_cast<i32x4*>(p.a.codes + code_place(p, row + piece % RB, cp)) = *reinterpret_cast<const i32x4*>(stage[threadIdx.x >> 6] + piece * 16);
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int k = 0; k < GROUP / 2; ++k) {
+          const int piece = k * 64 + lane, c = (j * tpr + t - lane) * 8 + piece / GROUP * 16;
+          if (c < 8 * p.chunks)
+            *reinterpret_cast<i32x4*>(p.a.codes + code_place(p, row0 + piece % GROUP, c)) =
+                *reinterpret_cast<const i32x4*>(stage + (wave * CH + j) * 512 * GROUP + piece * 16);
         }
-        __builtin_amdgcn_wave_barrier();
-      }
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
@@ -255,11 +235,11 @@ __device__ __forceinline__ void load_total(const FwdParams& p, int64_t row, int6
 template <class T, bool CODES>
 __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
   constexpr int TPR = 1024;
-  __shared__ double buf[2][1][TPR / 64];
+  __shared__ double buf[2][TPR / 64];
   const int rows = CODES ? p.padded_rows : p.tokens;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-    double s[1] = {0.0};
+    double s = 0.0;
     if (row < p.tokens) {
       float q = 0.0f;
       for (int64_t c = 8 * threadIdx.x; c < p.features; c += 8 * TPR) {
@@ -268,10 +248,10 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) q += v[i] * v[i];
       }
-      s[0] = q;
+      s = q;
     }
-    row_sums<TPR, 1>(s, buf, turn);
-    const double r = inverse_root(s[0] / p.features + static_cast<double>(p.eps));
+    s = row_sum<false, TPR>(s, buf, turn);
+    const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
     const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
     if (p.a.rstd && threadIdx.x == 0 && row < p.tokens) p.a.rstd[row] = hi;
     for (int64_t c = 8 * threadIdx.x; c < 8 * static_cast<int64_t>(p.chunks); c += 8 * TPR) {
@@ -296,84 +276,63 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
   }
 }
 
-// RB rows at a time, whose loads are on their way together.  SAME: dy has
-// total's type.
-template <class T, bool SAME, int TPR, int CH, int RB>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdParams p) {
-  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float buf[2][RB][TPR / 64];
-  const int t = threadIdx.x % TPR;
+// SAME: dy has total's type.
+template <class T, bool SAME, bool WAVE, int MOST, int CH>
+__global__ __launch_bounds__(MOST) void k_norm_bwd(const BwdParams p) {
+  const int tpr = WAVE ? 64 : blockDim.x;
+  constexpr int RPW = WAVE ? MOST / 64 : 1;
+  __shared__ float buf[2][MOST / 64];
+  const int t = WAVE ? threadIdx.x & 63 : threadIdx.x, group = WAVE ? threadIdx.x >> 6 : 0;
   float w[CH][8], dw[CH][8];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    load_any(p.a.weight, p.a.w_dtype, 0, (j * TPR + t) * 8, p.features, w[j]);
+    load_any(p.a.weight, p.a.w_dtype, 0, (j * tpr + t) * 8, p.features, w[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = (static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR) * RB; row < p.tokens;
-       row += static_cast<int64_t>(gridDim.x) * RPW * RB, turn ^= 1) {
-    Raw8<T> gr[RB][CH], hr[RB][CH], dr[RB][CH];
-    float r[RB], s[RB];
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + group; row < p.tokens; row += static_cast<int64_t>(gridDim.x) * RPW, turn ^= 1) {
+    Raw8<T> gr[CH], hr[CH], dr[CH];
+    const float r = p.a.rstd[row];
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const int cols = row + b < p.tokens ? p.features : 0;
-      r[b] = row + b < p.tokens ? p.a.rstd[row + b] : 0.0f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        const int c = (j * TPR + t) * 8;
-        if constexpr (SAME) gr[b][j] = load_raw8(static_cast<const T*>(p.a.dy) + (row + b) * p.a.lddy, c, cols);
-        hr[b][j] = load_raw8(static_cast<const T*>(p.a.total) + (row + b) * p.a.ldt, c, cols);
-        dr[b][j] = {};
-        if (p.a.dtotal) dr[b][j] = load_raw8(static_cast<const T*>(p.a.dtotal) + (row + b) * p.a.lddt, c, cols);
-      }
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * tpr + t) * 8;
+      if constexpr (SAME) gr[j] = load_raw8(static_cast<const T*>(p.a.dy) + row * p.a.lddy, c, p.features);
+      hr[j] = load_raw8(static_cast<const T*>(p.a.total) + row * p.a.ldt, c, p.features);
+      dr[j] = {};
+      if (p.a.dtotal) dr[j] = load_raw8(static_cast<const T*>(p.a.dtotal) + row * p.a.lddt, c, p.features);
     }
-    // dy, h and the sum of g h; g and h are computed again below, which takes fewer registers than keeping them
-    auto terms = [&](int b, int j, float* dy, float* h) {
-      const int c = (j * TPR + t) * 8;
-      if constexpr (SAME) unpack8(gr[b][j], dy);
-      else load_any(p.a.dy, p.a.dy_dtype, (row + b) * p.a.lddy, c, row + b < p.tokens ? p.features : 0, dy);
-      unpack8(hr[b][j], h);
+    float g[CH][8], h[CH][8], s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] *= r[b];
-    };
+    for (int j = 0; j < CH; ++j) {
+      if constexpr (SAME) unpack8(gr[j], g[j]);
+      else load_any(p.a.dy, p.a.dy_dtype, row * p.a.lddy, (j * tpr + t) * 8, p.features, g[j]);
+      unpack8(hr[j], h[j]);
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      s[b] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        float dy[8], h[8];
-        terms(b, j, dy, h);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[j][i] += dy[i] * h[i];
-          s[b] += (dy[i] * w[j][i]) * h[i];
-        }
+      for (int i = 0; i < 8; ++i) {
+        h[j][i] *= r;
+        dw[j][i] += g[j][i] * h[j][i];
+        g[j][i] *= w[j][i];
+        s += g[j][i] * h[j][i];
       }
     }
     if (!p.a.dx) continue;
-    row_sums<TPR, RB>(s, buf, turn);
+    const float m = row_sum<WAVE, MOST>(s, buf, turn) / static_cast<float>(p.features);
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (row + b >= p.tokens) break;
-      const float m = s[b] / static_cast<float>(p.features);
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * tpr + t) * 8;
+      float d[8];
+      unpack8(dr[j], d);
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        const int c = (j * TPR + t) * 8;
-        float dy[8], h[8], d[8];
-        terms(b, j, dy, h);
-        unpack8(dr[b][j], d);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] += r[b] * (dy[i] * w[j][i] - h[i] * m);
-        if (c < p.features) store_row8(static_cast<T*>(p.a.dx) + (row + b) * p.a.lddx, c, p.features, d);
-      }
+      for (int i = 0; i < 8; ++i) d[i] += r * (g[j][i] - h[j][i] * m);
+      if (c < p.features) store_row8(static_cast<T*>(p.a.dx) + row * p.a.lddx, c, p.features, d);
     }
   }
   if (!p.partial) return;
   if constexpr (RPW > 1) {
     // the workgroup's waves in their order
-    __shared__ float sum[RPW][TPR * 8 + 8];
-    const int rw = threadIdx.x / TPR;
+    __shared__ float sum[RPW][64 * 8 + 8];
+    const int rw = group;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       __syncthreads();
@@ -390,7 +349,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdPar
   }
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
-    const int c = (j * TPR + t) * 8;
+    const int c = (j * tpr + t) * 8;
     if (c < p.features) store_row8(p.partial + static_cast<int64_t>(blockIdx.x) * p.features, c, p.features, dw[j]);
   }
 }
@@ -398,13 +357,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdPar
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
   constexpr int TPR = 1024;
-  __shared__ float buf[2][1][TPR / 64];
+  __shared__ float buf[2][TPR / 64];
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.tokens; row += gridDim.x, turn ^= 1) {
     const float r = p.a.rstd[row];
     float m = 0.0f;
     for (int pass = 0; pass < 2; ++pass) {
-      float s[1] = {0.0f};
+      float s = 0.0f;
       for (int64_t c = 8 * threadIdx.x; c < p.features; c += 8 * TPR) {
         float g[8], h[8], w[8];
         load_any(p.a.dy, p.a.dy_dtype, row * p.a.lddy, c, p.features, g);
@@ -414,7 +373,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
         for (int i = 0; i < 8; ++i) {
           h[i] *= r;
           g[i] *= w[i];
-          s[0] += g[i] * h[i];
+          s += g[i] * h[i];
         }
         if (pass == 0) continue;
         float d[8] = {};
@@ -423,10 +382,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd_long(const BwdParams p) {
         for (int i = 0; i < 8; ++i) d[i] += r * (g[i] - h[i] * m);
         store_row8(static_cast<T*>(p.a.dx) + row * p.a.lddx, c, p.features, d);
       }
-      if (pass == 0) {
-        row_sums<TPR, 1>(s, buf, turn);
-        m = s[0] / static_cast<float>(p.features);
-      }
+      if (pass == 0) m = row_sum<false, TPR>(s, buf, turn) / static_cast<float>(p.features);
     }
   }
 }
@@ -468,34 +424,43 @@ __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ 
   }
 }
 
-// Threads of a row of `chunks` pieces, which they hold in registers, 1 or 2 each,
-// or 0 where those are too few.
-int threads_per_row(int64_t chunks) { return chunks <= 128 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? 512 : chunks <= 2048 ? 1024 : 0; }
-
-// Rows that a thread has in registers at a time: one of few rows, so that they
-// are spread over the CUs, and one where 1024 threads leave it 128 registers.
-constexpr int kManyRows = 1024;
-constexpr int rows_at_once(int tpr, bool bwd) { return tpr == 1024 ? 1 : bwd ? 2 : 4; }
-
-// Workgroups: enough for all CUs to be full, then each takes more rows.  (Of the
-// backward pass all read partial sums of the weight's gradient are read again.)
-int norm_groups(int64_t rows, int tpr, int at_once, bool bwd) {
-  const int64_t per = (tpr == 64 ? 4 : 1) * at_once, n = (rows + per - 1) / per;
-  return static_cast<int>(std::min<int64_t>(n, bwd || tpr == 1024 ? 512 : 2048));
+// How a row of `chunks` pieces is held in registers.
+struct Layout {
+  bool wave;    // by a wave, four rows of a workgroup; else by the workgroup
+  int threads;  // of a workgroup; 0: it is not, and read twice
+  int pieces;   // of a thread
+  int most;     // threads that the kernel is made for
+};
+Layout layout(int64_t chunks) {
+  if (chunks <= 128) return {true, 256, chunks <= 64 ? 1 : 2, 256};
+  if (chunks > 2048) return {false, 0, 0, 0};
+  const int pieces = chunks <= 256 ? 1 : 2;
+  const int threads = static_cast<int>((chunks + 64 * pieces - 1) / (64 * pieces) * 64);
+  return {false, threads, pieces, threads <= 512 ? 512 : 1024};
 }
 
-// go(threads per row, pieces of a thread) as compile-time constants
+// Rows whose codes are written together: not of few rows, which are spread over
+// the CUs.
+int rows_together(int64_t tokens) { return tokens >= 1024 ? 4 : 1; }
+
+// Workgroups: enough for all CUs to be full, then each takes more rows.  (Of the
+// backward pass all write partial sums of the weight's gradient, which are read
+// again.)
+int norm_groups(int64_t rows, const Layout& l, int together, bool bwd) {
+  const int64_t per = (l.wave ? 4 : 1) * together, n = (rows + per - 1) / per;
+  return static_cast<int>(std::min<int64_t>(n, bwd || l.most == 1024 ? 512 : 2048));
+}
+
+// go(whether a wave has a row, threads, pieces) as compile-time constants
 template <class F>
-void by_size(int64_t chunks, F&& go) {
-  const int tpr = threads_per_row(chunks);
-  auto with = [&](auto t) {
-    if (chunks <= decltype(t)::value) go(t, std::integral_constant<int, 1>{});
-    else go(t, std::integral_constant<int, 2>{});
+void by_layout(const Layout& l, F&& go) {
+  auto with = [&](auto wave, auto most) {
+    if (l.pieces == 1) go(wave, most, std::integral_constant<int, 1>{});
+    else go(wave, most, std::integral_constant<int, 2>{});
   };
-  if (tpr == 64) with(std::integral_constant<int, 64>{});
-  else if (tpr == 256) with(std::integral_constant<int, 256>{});
-  else if (tpr == 512) with(std::integral_constant<int, 512>{});
-  else with(std::integral_constant<int, 1024>{});
+  if (l.wave) with(std::true_type{}, std::integral_constant<int, 256>{});
+  else if (l.most == 512) with(std::false_type{}, std::integral_constant<int, 512>{});
+  else go(std::false_type{}, std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 
 template <class F>
@@ -504,6 +469,9 @@ void by_type(mx_dtype t, F&& go) {
   else if (t == MX_F16) go(f16_t{});
   else go(float{});
 }
+
+// Workgroups of the backward pass, whose partial sums the workspace holds.
+int bwd_groups(const mx_norm_desc& d) { return norm_groups(d.tokens, layout((static_cast<int64_t>(d.features) + 7) / 8), 1, true); }
 
 }  // namespace
 
@@ -519,29 +487,26 @@ hipError_t launch_norm_fwd(const mx_norm_desc& d, const NormFwd& a, hipStream_t 
   p.chunks = static_cast<int>(codes ? pad128(d.features) / 8 : (static_cast<int64_t>(d.features) + 7) / 8);
   const int64_t rows = codes ? p.padded_rows : p.tokens;
   if (rows == 0) return hipSuccess;
+  const Layout l = layout(p.chunks);
   by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    if (threads_per_row(p.chunks) == 0) {
-      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(norm_groups(rows, 1024, 1, false)), dim3(1024), 0, s, p); };
+    if (l.threads == 0) {
+      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(norm_groups(rows, l, 1, false)), dim3(1024), 0, s, p); };
       codes ? go(k_norm_fwd_long<T, true>) : go(k_norm_fwd_long<T, false>);
-    } else by_size(p.chunks, [&](auto n, auto ch) {
-      constexpr int N = decltype(n)::value, C = decltype(ch)::value, R = rows_at_once(N, false);
-      auto go = [&](auto kern, int at_once) { hipLaunchKernelGGL(kern, dim3(norm_groups(rows, N, at_once, false)), dim3(N < 256 ? 256 : N), 0, s, p); };
-      if (d.tokens >= kManyRows) codes ? go(k_norm_fwd<T, N, C, R, true>, R) : go(k_norm_fwd<T, N, C, R, false>, R);
-      else codes ? go(k_norm_fwd<T, N, C, 1, true>, 1) : go(k_norm_fwd<T, N, C, 1, false>, 1);
+    } else by_layout(l, [&](auto wave, auto most, auto pieces) {
+      constexpr bool W = decltype(wave)::value;
+      constexpr int M = decltype(most)::value, C = decltype(pieces)::value;
+      auto go = [&](auto kern, int together) {
+        const size_t lds = together > 1 ? static_cast<size_t>(l.threads / 64 * C * 512 * together) : 0;
+        hipLaunchKernelGGL(kern, dim3(norm_groups(rows, l, together, false)), dim3(l.threads), lds, s, p);
+      };
+      if (!codes) go(k_norm_fwd<T, W, M, C, false, 1>, 1);
+      else if (rows_together(d.tokens) == 4) go(k_norm_fwd<T, W, M, C, true, 4>, 4);
+      else go(k_norm_fwd<T, W, M, C, true, 1>, 1);
     });
   });
   return hipGetLastError();
 }
-
-namespace {
-// Workgroups of the backward pass, whose partial sums the workspace holds: no
-// more than with one row at a time.
-int bwd_groups(const mx_norm_desc& d) {
-  const int tpr = threads_per_row((static_cast<int64_t>(d.features) + 7) / 8);
-  return norm_groups(d.tokens, tpr ? tpr : 1024, 1, true);
-}
-}  // namespace
 
 size_t norm_workspace(const mx_norm_desc& d) {
   return d.tokens == 0 ? 0 : sizeof(float) * static_cast<size_t>(bwd_groups(d)) * static_cast<size_t>(d.features);
@@ -554,22 +519,19 @@ hipError_t launch_norm_bwd(const mx_norm_desc& d, const NormBwd& a, void* worksp
   p.features = d.features;
   p.partial = a.dweight && d.tokens > 0 ? static_cast<float*>(workspace) : nullptr;
   const int64_t chunks = (static_cast<int64_t>(d.features) + 7) / 8;
-  int groups = bwd_groups(d);
+  const Layout l = layout(chunks);
+  const int groups = bwd_groups(d);
   if (d.tokens > 0) by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    if (threads_per_row(chunks) == 0) {
+    if (l.threads == 0) {
       // (first, since dx may be in dy's place)
       if (p.partial) hipLaunchKernelGGL(k_norm_dweight<T>, dim3(static_cast<unsigned>((chunks + 255) / 256), groups), dim3(256), 0, s, p);
       if (a.dx) hipLaunchKernelGGL(k_norm_bwd_long<T>, dim3(groups), dim3(1024), 0, s, p);
-    } else by_size(chunks, [&](auto n, auto ch) {
-      constexpr int N = decltype(n)::value, C = decltype(ch)::value, R = rows_at_once(N, true);
-      auto go = [&](auto kern, int at_once) {
-        groups = norm_groups(d.tokens, N, at_once, true);
-        hipLaunchKernelGGL(kern, dim3(groups), dim3(N < 256 ? 256 : N), 0, s, p);
-      };
-      if (a.dy_dtype != a.dtype) go(k_norm_bwd<T, false, N, C, 1>, 1);
-      else if (d.tokens >= kManyRows) go(k_norm_bwd<T, true, N, C, R>, R);
-      else go(k_norm_bwd<T, true, N, C, 1>, 1);
+    } else by_layout(l, [&](auto wave, auto most, auto pieces) {
+      constexpr bool W = decltype(wave)::value;
+      constexpr int M = decltype(most)::value, C = decltype(pieces)::value;
+      auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(groups), dim3(l.threads), 0, s, p); };
+      a.dy_dtype == a.dtype ? go(k_norm_bwd<T, true, W, M, C>) : go(k_norm_bwd<T, false, W, M, C>);
     });
   });
   if (a.dweight)
