@@ -256,6 +256,20 @@ LinVariant variant(const Plan& pl) {
   return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
 }
 
+// Tiles and split by estimated time, in us, fitted to measured products (64 to
+// 16384 rows, 512 to 8192 columns).  A round is 256 workgroups, one per CU; each
+// step of 128 columns takes twice as long with exact products.
+//   Big    9 for the first loads and the stores, 13 of fp32 outputs, 1.4 per step
+//          and round, bound by the MFMA (4096^3 54, Small 63, Tiny 99; exact 104,
+//          114, 149; the weight gradients of 16 experts' 1024 tokens, 2048x2048,
+//          exact 144, Small 131)
+//   Small  5, and 0.5 per step and round, bound by L2 (2048^3 13.4, Tiny 19, Big 26)
+//   Tiny   3.6, and 0.24 per step and round, bound by the latency of a step
+//          (301x2500x1999 8.5, Small 12; 512x4096x4096 17.4, Small 18.3)
+// Splitting the contraction costs a launch, 3, and the traffic of its partial
+// sums at 4 TB/s: it pays for long contractions with few outputs (256x1024x4096
+// exact 14 in 4 pieces, 19 whole; without exact products 11.6 either way).  Tiles
+// too small for a launch's 2^32 - 1 threads are left out, as in 4 bits.
 Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
   const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;
@@ -280,7 +294,7 @@ Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
     pl.splits = pieces > 1 ? static_cast<int>((all_steps + pl.split_steps - 1) / pl.split_steps) : 1;
     const int64_t likely = pl.units - extra * pl.tiles_j / 2;
     const double rounds = static_cast<double>((likely * pl.splits + 255) / 256), each = steps / pl.splits * (exact ? 2 : 1);
-    double time = shape == 2 ? rounds * (9.0 + 1.4 * each) : shape == 1 ? 5.0 + rounds * 0.5 * each : 3.6 + rounds * 0.24 * each;
+    double time = shape == 2 ? rounds * ((exact ? 13.0 : 9.0) + 1.4 * each) : shape == 1 ? 5.0 + rounds * 0.5 * each : 3.6 + rounds * 0.24 * each;
     if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
     const LinVariant v = variant(pl);
     if (v.workgroups * v.threads > std::numeric_limits<uint32_t>::max()) return;
