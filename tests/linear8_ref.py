@@ -17,30 +17,28 @@ def round_e4m3(v):
 
 def exponent(top):
     """The smallest e >= -127 with top <= 448 * 2^e."""
-    if top == 0:
-        return -127
-    e = int(np.frexp(top)[1]) - 9  # 448 = 0.875 * 2^9
-    while top > np.ldexp(448.0, e):
-        e += 1
-    while top <= np.ldexp(448.0, e - 1):
-        e -= 1
-    return max(e, -127)
+    e = np.frexp(top)[1] - 9  # 448 = 0.875 * 2^9
+    e = e + (top > np.ldexp(448.0, e))
+    return np.where(top == 0, -127, np.maximum(e, -127))
 
 
 def quantize(x, rows: int, cols: int):
     """(values on the grid, scale code of each element) of x in float64, in
     blocks of rows x cols counted from the first element."""
-    val, code = np.zeros(x.shape), np.zeros(x.shape, np.uint8)
-    for i in range(0, x.shape[0], rows):
-        for j in range(0, x.shape[1], cols):
-            b = x[i:i + rows, j:j + cols]
-            s = (slice(i, i + b.shape[0]), slice(j, j + b.shape[1]))
-            if not np.isfinite(b).all():
-                val[s], code[s] = np.nan, 255
-                continue
-            e = exponent(np.abs(b).max())
-            val[s], code[s] = np.ldexp(round_e4m3(np.ldexp(b, -e)), e), e + 127
-    return val, code
+    r, c = x.shape
+    if x.size == 0:
+        return np.zeros((r, c)), np.zeros((r, c), np.uint8)
+    b = np.pad(x, ((0, -r % rows), (0, -c % cols)))
+    b = b.reshape(b.shape[0] // rows, rows, b.shape[1] // cols, cols)
+    finite = np.isfinite(b).all(axis=(1, 3), keepdims=True)
+    b = np.where(finite, b, 0.0)
+    e = exponent(np.abs(b).max(axis=(1, 3), keepdims=True))
+    val = np.where(finite, np.ldexp(round_e4m3(np.ldexp(b, -e)), e), np.nan)
+    code = np.broadcast_to(np.where(finite, e + 127, 255), b.shape).astype(np.uint8)
+
+    def back(a):
+        return a.reshape(a.shape[0] * rows, -1)[:r, :c]
+    return back(val), back(code)
 
 
 def form(x, block: int, f: int):

@@ -83,7 +83,7 @@ def forward_case(m, k, dt, ydt, wdt, seed=1, pad=0, residual=True, in_place=None
     assert all(torch.equal(a, b) for a, b in zip(q.buffers[0], q2.buffers[0]))
 
 
-# one, two and four pieces of 64 and 256 threads, one and two of 1024, rows read twice; odd lengths at each border
+# a wave's rows and a workgroup's of up to 512 and 1024 threads, one and two pieces each, rows read twice; odd lengths at each border
 LENGTHS = [1, 7, 8, 127, 129, 511, 513, 1000, 1024, 1025, 2048, 2049, 4096, 4100, 8192, 8193, 16384, 16385, 33000]
 
 
@@ -95,7 +95,7 @@ def test_forward(k):
         forward_case(3, k, dt, dt, "f32", residual=False)
 
 
-@pytest.mark.parametrize("m,k", [(1, 4096), (127, 300), (128, 256), (129, 1500), (5000, 70), (2100, 1100), (700, 9000), (600, 17000)])
+@pytest.mark.parametrize("m,k", [(1, 4096), (127, 300), (128, 256), (129, 1500), (5000, 70), (2100, 1100), (1100, 5000), (1030, 9000), (1025, 16300), (600, 17000)])
 def test_forward_many_rows(m, k):
     """More rows than workgroups, and borders of the 8-bit form's 128 rows."""
     say("forward", m, k)
