@@ -200,9 +200,8 @@ __global__ __launch_bounds__(256) void k_route_gather(const MoveParams p) {
   }
 }
 
-constexpr int kLoads = 4;  // choices whose loads are on their way together
-
-template <class T, bool WEIGHTED>
+// N: choices whose loads are on their way together.
+template <class T, bool WEIGHTED, int N>
 __global__ __launch_bounds__(256) void k_route_combine(const MoveParams p) {
   const int per = 256 >> p.lanes, l = threadIdx.x & ((1 << p.lanes) - 1);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (threadIdx.x >> p.lanes); t < p.tokens; t += static_cast<int64_t>(gridDim.x) * per) {
@@ -210,19 +209,19 @@ __global__ __launch_bounds__(256) void k_route_combine(const MoveParams p) {
     const float* weight = WEIGHTED ? p.weight + t * p.choices : nullptr;
     for (int64_t c = static_cast<int64_t>(l) * 8; c < p.features; c += 8 << p.lanes) {
       float s[8] = {};
-      for (int j0 = 0; j0 < p.choices; j0 += kLoads) {
-        Raw8<T> raw[kLoads];
-        bool has[kLoads];
-        float w[kLoads];
+      for (int j0 = 0; j0 < p.choices; j0 += N) {
+        Raw8<T> raw[N];
+        bool has[N];
+        float w[N];
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < N; ++j) {
           const int q = min(j0 + j, p.choices - 1), r = rows[q];
           has[j] = j0 + j < p.choices && static_cast<uint32_t>(r) < static_cast<uint32_t>(p.limit);
           raw[j] = load_raw8(static_cast<const T*>(p.a) + (has[j] ? r : 0) * p.lda, c, has[j] ? p.features : 0);
           w[j] = WEIGHTED ? weight[q] : 1.0f;
         }
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < N; ++j) {
           float v[8];
           unpack8(raw[j], v);
 #pragma unroll
@@ -235,36 +234,38 @@ __global__ __launch_bounds__(256) void k_route_combine(const MoveParams p) {
   }
 }
 
-constexpr int kAtOnce = 4;  // choices whose rows are read, and sums held, together
-
-template <class T>
+// N: choices whose rows are read, and sums held, together.  GROUP: a token is the
+// workgroup's, whose waves join their sums in LDS; else a wave's or less.
+template <class T, int N, bool GROUP>
 __global__ __launch_bounds__(256) void k_route_combine_bwd(const MoveParams p) {
-  const int per = 256 >> p.lanes, width = 1 << p.lanes, l = threadIdx.x & (width - 1);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (threadIdx.x >> p.lanes); t < p.tokens; t += static_cast<int64_t>(gridDim.x) * per) {
+  __shared__ float part[2][N][4];
+  const int lanes = GROUP ? 8 : p.lanes, per = 256 >> lanes, width = 1 << lanes, l = threadIdx.x & (width - 1);
+  int turn = 0;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * per + (threadIdx.x >> lanes); t < p.tokens; t += static_cast<int64_t>(gridDim.x) * per) {
     const T* dout = static_cast<const T*>(p.a) + t * p.lda;
-    for (int j0 = 0; j0 < p.choices; j0 += kAtOnce) {
-      int r[kAtOnce];
-      float w[kAtOnce], s[kAtOnce];
+    for (int j0 = 0; j0 < p.choices; j0 += N, turn ^= 1) {
+      int r[N];
+      float w[N], s[N];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < N; ++j) {
         const bool in = j0 + j < p.choices;
         r[j] = in ? p.rows[t * p.choices + j0 + j] : -1;
         if (static_cast<uint32_t>(r[j]) >= static_cast<uint32_t>(p.limit)) r[j] = -1;
         w[j] = in ? p.weight[t * p.choices + j0 + j] : 0.0f;
         s[j] = 0.0f;
       }
-      for (int64_t c = static_cast<int64_t>(l) * 8; c < p.features; c += 8 << p.lanes) {
+      for (int64_t c = static_cast<int64_t>(l) * 8; c < p.features; c += 8 << lanes) {
         const Raw8<T> graw = load_raw8(dout, c, p.features);
-        Raw8<T> yraw[kAtOnce];
+        Raw8<T> yraw[N];
         if (p.dweight) {
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j)
-            if (j0 + j < p.choices) yraw[j] = load_raw8(static_cast<const T*>(p.y) + max(r[j], 0) * p.ldy, c, r[j] < 0 ? 0 : p.features);
+          for (int j = 0; j < N; ++j)
+            yraw[j] = load_raw8(static_cast<const T*>(p.y) + max(r[j], 0) * p.ldy, c, r[j] < 0 ? 0 : p.features);
         }
         float g[8];
         unpack8(graw, g);
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < N; ++j) {
           if (r[j] < 0) continue;
           if (p.dweight) {
             float v[8];
@@ -282,9 +283,22 @@ __global__ __launch_bounds__(256) void k_route_combine_bwd(const MoveParams p) {
       }
       if (p.dweight) {
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          for (int d = 1; d < width; d *= 2) s[j] += __shfl_xor(s[j], d);
-          if (l == 0 && j0 + j < p.choices) p.dweight[t * p.choices + j0 + j] = s[j];
+        for (int j = 0; j < N; ++j)
+          for (int d = 1; d < min(width, 64); d *= 2) s[j] += __shfl_xor(s[j], d);
+        if constexpr (GROUP) {
+          // (the halves of `part` are used in turn: a wave that writes one again
+          // has passed the barrier between)
+          if ((l & 63) == 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) part[turn][j][l >> 6] = s[j];
+          }
+          __syncthreads();
+          if (l < N && j0 + l < p.choices)
+            p.dweight[t * p.choices + j0 + l] = (part[turn][l][0] + part[turn][l][1]) + (part[turn][l][2] + part[turn][l][3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (l == 0 && j0 + j < p.choices) p.dweight[t * p.choices + j0 + j] = s[j];
         }
       }
     }
@@ -313,6 +327,15 @@ SortParams make_sort(const mx_route_desc& d) {
   const int64_t each = (static_cast<int64_t>(p.n) + p.groups - 1) / p.groups;
   p.chunk = static_cast<int>((each + round - 1) / round * round);
   return p;
+}
+
+// go(choices that are taken together) as a compile-time constant: registers of
+// choices that there are not would leave fewer waves on a CU
+template <class F>
+void by_choices(int choices, F&& go) {
+  if (choices == 1) go(std::integral_constant<int, 1>{});
+  else if (choices == 2) go(std::integral_constant<int, 2>{});
+  else go(std::integral_constant<int, 4>{});
 }
 
 template <class F>
@@ -381,7 +404,10 @@ hipError_t launch_route_combine(const mx_route_desc& d, const void* y, int64_t l
   by_type(dtype, [&](auto t) {
     using T = decltype(t);
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(move_groups(p)), dim3(256), 0, s, p); };
-    weight ? go(k_route_combine<T, true>) : go(k_route_combine<T, false>);
+    by_choices(d.choices, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      weight ? go(k_route_combine<T, true, N>) : go(k_route_combine<T, false, N>);
+    });
   });
   return hipGetLastError();
 }
@@ -404,10 +430,16 @@ hipError_t launch_route_combine_bwd(const mx_route_desc& d, const void* dout, in
   p.choices = d.choices;
   p.features = d.features;
   p.limit = d.tokens * d.choices;
-  p.lanes = lanes_of((static_cast<int64_t>(d.features) + 7) / 8, 6);  // a wave at most, which adds its sums by itself
+  // a token is a wave's at most, or the workgroup's
+  p.lanes = lanes_of((static_cast<int64_t>(d.features) + 7) / 8, 8);
+  if (p.lanes == 7) p.lanes = 8;
   by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    hipLaunchKernelGGL(k_route_combine_bwd<T>, dim3(move_groups(p)), dim3(256), 0, s, p);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(move_groups(p)), dim3(256), 0, s, p); };
+    by_choices(d.choices, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      p.lanes == 8 ? go(k_route_combine_bwd<T, N, true>) : go(k_route_combine_bwd<T, N, false>);
+    });
   });
   return hipGetLastError();
 }
