@@ -10,8 +10,9 @@
  *     h  = total * rstd,  g = dy * weight
  *     dx = rstd * (g - h * mean(g * h)) + dtotal      (x's and the residual's gradient alike)
  *     dweight = sum over the tokens of dy * h
- * Sums, h and g are fp32, each result is rounded once.  Sums have a fixed
- * order: results are bit-reproducible.
+ * Sums, h and g are fp32 or more, each result is rounded once.  Sums have a
+ * fixed order: results are bit-reproducible.  A row whose sum of squares
+ * overflows fp32 has an rstd of 0, as one with an Inf.
  *
  * Matrices are [tokens][features] with a row stride in elements, of any
  * alignment that the type has.  total may be x or the residual, and dx may be
@@ -50,7 +51,8 @@ mx_status mx_norm_fwd(const mx_norm_desc* desc, const void* x, int64_t ldx, cons
                       const void* weight, mx_dtype w_dtype, void* total, int64_t ldt, void* y, mx_dtype y_dtype, int64_t ldy,
                       const mx_linear_qtensor* yq, float* rstd, hipStream_t stream);
 
-/* Bytes of workspace of mx_norm_bwd (0 on an invalid descriptor). */
+/* Bytes of workspace of mx_norm_bwd (0 on an invalid descriptor).  A workspace
+ * serves one call at a time, in captured graphs too. */
 size_t mx_norm_workspace_bytes(const mx_norm_desc* desc);
 
 /* The gradients.

@@ -48,7 +48,8 @@ typedef struct {
 /* MX_ERR_SHAPE: a value outside these, or tokens * choices of 2^30 or more. */
 
 /* Bytes of workspace of mx_route_sort (0 on an invalid descriptor, or where
- * none is needed). */
+ * none is needed).  A workspace serves one call at a time, in captured graphs
+ * too. */
 size_t mx_route_workspace_bytes(const mx_route_desc* desc);
 
 /* expert [tokens][choices] -> offsets [experts + 1], rows [tokens][choices] and,

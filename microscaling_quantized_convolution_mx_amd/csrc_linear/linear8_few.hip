@@ -14,6 +14,11 @@
 // The codes are widened to bf16 with their scales, and the products are exact
 // whatever the output's type: the matrix units have time for that while w
 // arrives.  Tokens quantized here are kept in LDS as bf16.
+//
+// Measured in graphs of such calls, which leave the weight in the last-level
+// cache: 1x16384x8192 22.8 us (5.9 TB/s of weight) or, quantizing, 24.6,
+// 1x4096x4096 5.7 and 5.5 (128 workgroups: half of the CUs), 256 tokens of 64
+// experts, 2048x2048, 42 (6.4 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -33,7 +38,9 @@ constexpr size_t kTokenLds = size_t{64} << 10;  // for a pass' tokens in bf16: t
 template <class TX, int SN>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin8_few(const FewParams p) {
   constexpr bool kFused = !std::is_void_v<TX>;
-  // column tiles of a wave on their way, in half of the registers
+  // column tiles of a wave on their way, in half of the registers (1x4096x4096
+  // quantizing 5.4 us, 7.6 with 6 of them, 5.8 with 8 in all registers; not
+  // quantizing 5.7, 7.3 with 4, which spill)
   constexpr int kAhead = SN == 1 ? kFused ? 4 : 3 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, threads = blockDim.x;

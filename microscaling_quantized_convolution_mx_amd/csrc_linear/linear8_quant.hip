@@ -8,7 +8,13 @@
 // together in LDS, the column form's transposed by the lanes' 8 rows, and
 // written as whole stripes.
 //
-// Bound by memory traffic.
+// Bound by memory traffic: 16384x8192 bf16 76 us for the row form (5.3 TB/s, a
+// large copy's rate), 79 for the column form, 107 for both (5.0); dequantizing
+// the row form to bf16 64 (6.3 TB/s, most of it stores past the caches), to fp32
+// 8192x8192 94.  The column form dequantizes at 3.3 TB/s: its bytes go through
+// LDS one by one.  A lane's 8 loads are issued before the first is converted;
+// each next to its conversion, in the branch for the row's end, both forms took
+// 133 us.
 #include <type_traits>
 
 #include "linear8_codes.h"

@@ -5,12 +5,19 @@
 //         dx = rstd (g - h mean(g h)) + dtotal,  dweight = sum over tokens of dy h
 //
 // Bound by memory traffic: everything is read and written once.  A row is held
-// in the registers of one wave, of 4 or of 16 (TPR threads), CH pieces of 8
-// elements each, between the sum over it and the results that need the sum.
+// in the registers of a wave or a workgroup, CH pieces of 8 elements of each
+// thread, between the sum over it and the results that need the sum.
 // Workgroups take rows in turn and keep the weight, and in the backward pass
 // the weight's gradient over their rows, in registers; those partial sums are
 // added by a second kernel in a fixed order.  Rows too long for registers are
 // read twice.
+//
+// Measured: 16384x4096 bf16 forward 104 us (5.1 TB/s, a large copy's rate),
+// backward 105 (5.1, the second kernel among it), 8192x8192 with the output in
+// 8 bits 103 (4.6); 16384x5000, rows that share cache lines, forward 139 (4.7), in
+// 8 bits 175 (3.3).  One row at a time fills the CUs better than several, whose
+// registers leave room for fewer waves (8192x8192 forward 101 us, 116 with 2 rows
+// at a time, 122 with 4).
 #include <algorithm>
 #include <type_traits>
 
@@ -139,7 +146,8 @@ __device__ __forceinline__ void add_residual(Raw8<T>& v, const Raw8<T>& r, float
 
 // Rows are taken GROUP at a time, one after the other.  With GROUP = 4 the codes
 // of 4 rows are written together, 64 consecutive bytes of 16 columns each: a
-// wave keeps its columns' codes in LDS of its own until it has all four.
+// wave keeps its columns' codes in LDS of its own until it has all four
+// (16384x4096 bf16 98 us, 131 with 8 bytes written at a time; 16384x1024 27 and 26).
 template <class T, bool WAVE, int MOST, int CH, bool CODES, int GROUP>
 __global__ __launch_bounds__(MOST) void k_norm_fwd(const FwdParams p) {
   const int tpr = WAVE ? 64 : blockDim.x;     // threads of a row

@@ -10,9 +10,13 @@
 // choices, without atomics.  Few choices are one workgroup's; for more, a first
 // kernel leaves each workgroup's counts and the second adds up those before it.
 //
+// 16384 tokens' 4 choices of 64 experts take 10 us, 32 tokens' 2 choices 3.5.
+//
 // Moves.  Bound by memory traffic: a token's row is read, or written, once for
 // all of its choices, and each of their rows once.  A token is some lanes' of a
-// workgroup, 16 bytes each at a time.
+// workgroup, 16 bytes each at a time.  16384 tokens of 4 choices, 2048 bf16
+// features: gather and its gradient 67 us (5.0 TB/s), combine 67, its gradient
+// 118 (5.1).  (A wave for each token: combine 84, its gradient 131.)
 #include <algorithm>
 #include <type_traits>
 
@@ -330,7 +334,9 @@ SortParams make_sort(const mx_route_desc& d) {
 }
 
 // go(choices that are taken together) as a compile-time constant: registers of
-// choices that there are not would leave fewer waves on a CU
+// choices that there are not would leave fewer waves on a CU (16384 tokens of 2
+// choices, 4096 features, combine 79 us, 89 with room for 4 and 184 for 8; 8
+// choices of 2048 features 120 by fours and 133 by eights)
 template <class F>
 void by_choices(int choices, F&& go) {
   if (choices == 1) go(std::integral_constant<int, 1>{});

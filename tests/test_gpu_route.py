@@ -269,6 +269,27 @@ def test_graph_stream_and_repeatability():
             assert torch.equal(a, b)
 
 
+def test_calls_at_once_on_two_streams():
+    """Sorts that run at once, with a workspace each."""
+    m, c, e = 40000, 4, 100
+    d = mx.route_desc(m, c, e, 1)
+    expert = [choices(s, m, c, e, 0.1) for s in (1, 2)]
+    want = [places(a, e) for a in expert]
+    given = [torch.from_numpy(a).to(DEV) for a in expert]
+    i32 = dict(dtype=torch.int32, device=DEV)
+    out = [(torch.empty(e + 1, **i32), torch.empty(m, c, **i32), torch.empty(m * c, **i32),
+            torch.empty(mx.mx_route_workspace_bytes(d), dtype=torch.uint8, device=DEV)) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, a, o in zip(streams, given, out):
+            mx.mx_route_sort(d, a, *o, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        for got, ref in zip(o, w):
+            same(got.cpu().numpy().reshape(ref.shape), ref)
+
+
 def test_matrices_past_32_bits():
     """Rows of more than 2^32 elements: the last tokens'."""
     m, c, k = 60000, 2, 40000
