@@ -25,7 +25,8 @@
 // of the time at 1.95 GHz of 2.4, in its weight gradient 74% at 1.86: power sets
 // the clock.  Neither another order of reads and copies between the MFMAs nor
 // more stages or slices between barriers changed these, the small tiles' times
-// neither (301x2500x1999 8.4 to 8.9, 2048^3 13.6 to 14.1).  Four rounds of 256 tiles
+// neither (301x2500x1999 8.4 to 8.9, 2048^3 13.6 to 14.1): their copies arrive at
+// some 60 bytes per ns and CU, half of what L2's width allows.  Four rounds of 256 tiles
 // cost about 9 us each for the first operands and the stores; overlapping these
 // with the tile before has not been measured.  Experts' products take 128x128 tiles
 // at the full clock, 33% busy, bound by L2: 16 experts of 2048x2048 with 16384 uneven
@@ -40,10 +41,19 @@
 namespace mx {
 namespace {
 
-// Big for the MFMA's rate, Tiny for short latency (make_plan).
-using Big = Shape<256, 256, 2, 2, 4>;
-using Small = Shape<128, 128, 2, 2, 4>;
-using Tiny = Shape<64, 64, 2, 2, 4>;
+// Big for the MFMA's rate, Tiny for short latency (make_plan).  kTeams: teams of
+// waves, each of which takes every kTeams-th slice of 64 columns for all of the
+// tile; their sums are joined at the end.
+template <int M, int N, int A, int B, int S, int G>
+struct Teams : Shape<M, N, A, B, S> {
+  static constexpr int kTeams = G, kThreads = 64 * A * B * G;
+};
+using Big = Teams<256, 256, 2, 2, 4, 1>;
+using Small = Teams<128, 128, 2, 2, 4, 1>;
+// (two teams of exact products, whose steps are twice as long: 301x2500x1999 10.9
+// us, 12.2 with one; other products 8.6 and 8.4, 512x4096x4096 19.3 and 18.0)
+template <bool EXACT>
+using Tiny = Teams<64, 64, 2, 2, 4, EXACT ? 2 : 1>;
 
 // Copies 16 (or 4) bytes per lane from src + off to the LDS address dst + lane *
 // 16 (4) without passing registers.  src and dst are the wave's.  The compiler
@@ -65,40 +75,43 @@ __device__ __forceinline__ void copy4_lds(const uint8_t* src, uint32_t off, uint
 // columns.  A tile's plane in LDS is read as it is, 64 lanes x 16 consecutive
 // bytes, which is free of bank conflicts.
 template <class T, class Shape, bool CONTRACT, bool EXACT>
-__global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(const ProductParams p) {
-  constexpr int TM = Shape::TM, TN = Shape::TN, WM = Shape::WM, WN = Shape::WN, kStages = Shape::kStages;
+__global__ __launch_bounds__(Shape::kThreads) void k_lin8_product(const ProductParams p) {
+  constexpr int TM = Shape::TM, TN = Shape::TN, WM = Shape::WM, WN = Shape::WN, kStages = Shape::kStages, kTeams = Shape::kTeams;
   constexpr int RM = TM / WM / 32, RN = TN / WN / 32;  // MFMA rows and columns of a wave
-  constexpr int kWaves = WM * WN;
-  constexpr int kOpndA = TM / 32 * k8TileBytes, kOpndB = TN / 32 * k8TileBytes;
+  constexpr int kTeam = WM * WN, kWaves = kTeam * kTeams;
+  static_assert(kTeams <= 2);
+  constexpr int kOpndA = TM / 32 * kTeams * k8TileBytes, kOpndB = TN / 32 * kTeams * k8TileBytes;
   // groups of 128 rows' scales (of which a tile of 64 uses half), each there twice: for lanes 0..31 and 32..63
   constexpr int kGroupsA = (TM + kPad - 1) / kPad, kGroups = kGroupsA + (TN + kPad - 1) / kPad;
   constexpr int kGroupBytes = 2 * k8ScaleBytes;
   constexpr int kScales = kOpndA + kOpndB;  // their place in a stage
   constexpr int kStage = kScales + kGroups * kGroupBytes;
-  constexpr int kStoreBytes = kWaves * store_bytes<T, RN>();
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage > kStoreBytes ? kStages * kStage : kStoreBytes];
+  constexpr int kSumBytes = RM * RN * 64 * static_cast<int>(sizeof(f32x16));  // of a wave's results
+  constexpr int kEndBytes = kTeam * (store_bytes<T, RN>() + (kTeams > 1 ? kSumBytes : 0));
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kStages * kStage > kEndBytes ? kStages * kStage : kEndBytes];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave % WM, wn = wave / WM;
+  const int team = wave / kTeam, wm = wave % WM, wn = wave % kTeam / WM;
   Work w;
   if (!find_work<TM, TN, CONTRACT, true>(p, w)) return;
-  const int nslices = 2 * w.nsteps;
+  const int nsteps = 2 / kTeams * w.nsteps;  // of a slice for each team
 
-  // Copies of a slice: copy l of wave w takes plane l * kWaves + w of a's tiles,
-  // then of b's, and then groups of scales.  A stripe past the operand's end is
-  // read as its last one: those outputs are not stored.
-  constexpr int kPlanesA = TM / 16 / kWaves, kPlanes = (TM + TN) / 16 / kWaves;
+  // Copies of a step: copy l of wave w takes plane l * kWaves + w of a's tiles
+  // (a stripe's follow each other in memory), then of b's, and then groups of
+  // scales.  A stripe past the operand's end is read as its last one: those
+  // outputs are not stored.
+  constexpr int kPlanesA = kTeams * TM / 16 / kWaves, kPlanes = kTeams * (TM + TN) / 16 / kWaves;
   constexpr int kScaleCopies = (kGroups + kWaves - 1) / kWaves, kCopies = kPlanes + kScaleCopies;
-  static_assert(TM / 16 % kWaves == 0 && TN / 16 % kWaves == 0);
+  static_assert(kTeams * TM / 16 % kWaves == 0 && kTeams * TN / 16 % kWaves == 0);
   const uint8_t *src[kPlanes], *ssrc[kScaleCopies];
   uint32_t sdst[kScaleCopies];
   static_for<kPlanes>([&](auto lc) {
     constexpr int L = decltype(lc)::value;
     constexpr bool of_b = L >= kPlanesA;
     const int i = (of_b ? L - kPlanesA : L) * kWaves + wave;
-    const int64_t st = min((of_b ? w.brow : w.arow) / kTileR + i / 2, (of_b ? p.b_rows : p.a_rows) / kTileR - 1);
-    src[L] = (of_b ? p.b : p.a) + (st * (of_b ? p.bkt : p.akt) + w.k0) * k8TileBytes + i % 2 * 1024;
+    const int64_t st = min((of_b ? w.brow : w.arow) / kTileR + i / (2 * kTeams), (of_b ? p.b_rows : p.a_rows) / kTileR - 1);
+    src[L] = (of_b ? p.b : p.a) + (st * (of_b ? p.bkt : p.akt) + w.k0) * k8TileBytes + i % (2 * kTeams) * 1024;
   });
   static_for<kScaleCopies>([&](auto lc) {
     constexpr int L = decltype(lc)::value;
@@ -109,18 +122,18 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(con
     sdst[L] = kScales + static_cast<uint32_t>(i) * kGroupBytes;
   });
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-  // copy l of the slice that the sources stand at, into the stage at `to`
+  // copy l of the step that the sources stand at, into the stage at `to`
   auto copy = [&](uint32_t to, auto l) {
     constexpr int L = decltype(l)::value;
     if constexpr (L < kPlanes) copy16_lds(src[L], lane * 16u, lds0 + to + (L * kWaves + wave) * 1024);
     else copy4_lds(ssrc[L - kPlanes], (lane & 31) * 4u, lds0 + to + sdst[L - kPlanes]);
   };
-  // to the next slice; two share their scales
+  // to the next step; two slices share their scales
   auto advance = [&](bool on, bool odd) {
     const int d = on ? 1 : 0;
 #pragma unroll
-    for (int q = 0; q < kPlanes; ++q) src[q] += d * k8TileBytes;
-    if (odd) {
+    for (int q = 0; q < kPlanes; ++q) src[q] += d * kTeams * k8TileBytes;
+    if (kTeams == 2 || odd) {
 #pragma unroll
       for (int i = 0; i < kScaleCopies; ++i) ssrc[i] += d * k8ScaleBytes;
     }
@@ -155,10 +168,10 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(con
       f.sb = read_scales(st + kScales + kGroupsA * kGroupBytes, sb0 + wn * RN, RN);
     } else if constexpr (R < 2 + 2 * RM) {
       constexpr int I = (R - 2) / 2, P = (R - 2) % 2;
-      f.a[I][P] = reinterpret_cast<const i32x4*>(st + (wm * RM + I) * k8TileBytes + P * 1024)[lane];
+      f.a[I][P] = reinterpret_cast<const i32x4*>(st + ((wm * RM + I) * kTeams + team) * k8TileBytes + P * 1024)[lane];
     } else {
       constexpr int I = (R - 2 - 2 * RM) / 2, P = (R - 2) % 2;
-      f.b[I][P] = reinterpret_cast<const i32x4*>(st + kOpndA + (wn * RN + I) * k8TileBytes + P * 1024)[lane];
+      f.b[I][P] = reinterpret_cast<const i32x4*>(st + kOpndA + ((wn * RN + I) * kTeams + team) * k8TileBytes + P * 1024)[lane];
     }
   };
   auto both = [](const i32x4 (&v)[2]) {
@@ -209,49 +222,74 @@ __global__ __launch_bounds__(64 * Shape::WM * Shape::WN) void k_lin8_product(con
     }
   };
 
-  // Slice s, on stage s%S of S, with its operands read during slice s-1:
-  //   multiply it, reading slice s+1 from its stage and copying slice s+S into
+  // Step s, on stage s%S of S, with its operands read during step s-1:
+  //   multiply it, reading step s+1 from its stage and copying step s+S into
   //   stage s%S, which every wave had read at the last barrier;
-  //   barrier: every wave has read slice s+1, and its copies of slice s+2 have
-  //   arrived (those of the S-2 slices after may be on their way).
+  //   barrier: every wave has read step s+1, and its copies of step s+2 have
+  //   arrived (those of the S-2 steps after may be on their way).
   // With one wave per SIMD nothing else hides an LDS access, so reads and
-  // copies are dealt out between the MFMAs.  Copies past the last slice repeat
-  // it, into stages that nothing reads.
-  if (nslices > 0) {
+  // copies are dealt out between the MFMAs.  Copies past the last step repeat it,
+  // into stages that nothing reads.
+  if (nsteps > 0) {
     static_for<kStages>([&](auto st) {
       constexpr int S = decltype(st)::value;
       static_for<kCopies>([&](auto l) { copy(S * kStage, l); });
-      advance(S + 1 < nslices, S % 2);
+      advance(S + 1 < nsteps, S % 2);
     });
     wait_barrier<(kStages - 2) * kCopies>();
     static_for<kReads>([&](auto r) {
       read(lds, fA, r);
       __builtin_amdgcn_sched_barrier(0);
     });
-    // (all have read slice 0: its stage is copied into from here on)
+    // (all have read step 0: its stage is copied into from here on)
     wait_barrier<(kStages - 2) * kCopies>();
     static_assert(kStages % 2 == 0);
     uint32_t cur = 0;
-    auto slice = [&](const Frags& f, Frags& g, int s, bool odd) {
+    auto step = [&](const Frags& f, Frags& g, int s, bool odd) {
       const uint32_t next = cur == (kStages - 1) * kStage ? 0 : cur + kStage;
       multiply(f, [&](auto n) {
         deal(n, Idx<kReads>{}, Idx<(kSlots * 3 + 3) / 4>{}, [&](auto r) { read(lds + next, g, r); });
         deal(n, Idx<kCopies>{}, Idx<kSlots>{}, [&](auto l) { copy(cur, l); });
       });
-      advance(s + kStages + 1 < nslices, odd);
+      advance(s + kStages + 1 < nsteps, odd);
       wait_barrier<(kStages - 2) * kCopies>();
       cur = next;
     };
-    for (int s = 0; s < nslices; s += 2) {
-      slice(fA, fB, s, false);
-      slice(fB, fA, s + 1, true);
+    for (int s = 0; s < nsteps; s += 2) {
+      step(fA, fB, s, false);
+      // (without teams the steps are even in number)
+      if (kTeams == 1 || s + 1 < nsteps) step(fB, fA, s + 1, true);
     }
     // the last copies have to land before the stores reuse LDS
     wait_barrier<0>();
   }
 
+  uint8_t* const sums = lds + kTeam * store_bytes<T, RN>();
+  if constexpr (kTeams == 2) {
+    // the second team's sums are added to the first's
+    f32x16* mine = reinterpret_cast<f32x16*>(sums) + static_cast<size_t>(wave % kTeam) * RM * RN * 64;
+    __syncthreads();
+    if (team == 1) {
+#pragma unroll
+      for (int i = 0; i < RM * RN; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          reinterpret_cast<f32x4*>(mine)[(i * 4 + v) * 64 + lane] = f32x4{acc[i / RN][i % RN][4 * v], acc[i / RN][i % RN][4 * v + 1], acc[i / RN][i % RN][4 * v + 2], acc[i / RN][i % RN][4 * v + 3]};
+    }
+    __syncthreads();
+    if (team == 1) return;
+#pragma unroll
+    for (int i = 0; i < RM * RN; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const f32x4 s = reinterpret_cast<const f32x4*>(mine)[(i * 4 + v) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i / RN][i % RN][4 * v + e] += s[e];
+      }
+  }
+
   T* tile = static_cast<T*>(p.out) + w.out + w.orow * p.ld + static_cast<int64_t>(w.tj) * TN;
-  uint8_t* buf = lds + wave * store_bytes<T, RN>();
+  uint8_t* buf = lds + wave % kTeam * store_bytes<T, RN>();
   if (p.stream) store_wave<true, RM, RN>(acc, buf, tile, p.ld, w.rleft, w.cleft, lane, wm, wn);
   else store_wave<false, RM, RN>(acc, buf, tile, p.ld, w.rleft, w.cleft, lane, wm, wn);
 }
@@ -263,9 +301,9 @@ struct Plan {
   int64_t units;  // workgroups, at most
 };
 
-LinVariant variant(const Plan& pl) {
-  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny::TM;
-  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : Tiny::kThreads;
+LinVariant variant(const Plan& pl, bool exact) {
+  const int size = pl.shape == 2 ? Big::TM : pl.shape == 1 ? Small::TM : Tiny<true>::TM;
+  const int threads = pl.shape == 2 ? Big::kThreads : pl.shape == 1 ? Small::kThreads : exact ? Tiny<true>::kThreads : Tiny<false>::kThreads;
   return {3, size, pl.splits, threads, (pl.units * pl.splits + 7) / 8 * 8};
 }
 
@@ -294,7 +332,7 @@ Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
   double best_time = 0.0;
   auto consider = [&](int shape, int64_t pieces) {
     Plan pl{};
-    const int tm = shape == 2 ? Big::TM : shape == 1 ? Small::TM : Tiny::TM, tn = shape == 2 ? Big::TN : shape == 1 ? Small::TN : Tiny::TN;
+    const int tm = shape == 2 ? Big::TM : shape == 1 ? Small::TM : Tiny<true>::TM, tn = shape == 2 ? Big::TN : shape == 1 ? Small::TN : Tiny<true>::TN;
     // every expert with tokens may leave a part of a tile more
     const int64_t extra = op != LIN_WGRAD && g.e > 0 ? used : 0;
     pl.shape = shape;
@@ -309,7 +347,7 @@ Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
     const double rounds = static_cast<double>((likely * pl.splits + 255) / 256), each = steps / pl.splits * (exact ? 2 : 1);
     double time = shape == 2 ? rounds * ((exact ? 13.0 : 9.0) + 1.4 * each) : shape == 1 ? 5.0 + rounds * 0.5 * each : 3.6 + rounds * 0.24 * each;
     if (pl.splits > 1) time += 3.0 + 8.0 * static_cast<double>(rows * cols) * pl.splits / 4e6;
-    const LinVariant v = variant(pl);
+    const LinVariant v = variant(pl, exact);
     if (v.workgroups * v.threads > std::numeric_limits<uint32_t>::max()) return;
     if (best.units == 0 || time < best_time) {
       best = pl;
@@ -327,7 +365,7 @@ Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
 LinVariant lin8_product_variant(const LinGeom& g, LinOp op, mx_dtype dtype) {
   if (op != LIN_WGRAD && g.m == 0) return {};
   if (op != LIN_WGRAD && lin8_few(g)) return lin8_few_variant(g, op == LIN_DGRAD, false);
-  return variant(make_plan(g, op, dtype == MX_F32));
+  return variant(make_plan(g, op, dtype == MX_F32), dtype == MX_F32);
 }
 
 // Whether the product writes past the caches: the rule of the products in 4
@@ -386,7 +424,7 @@ hipError_t launch_lin8_product(const LinGeom& g, LinOp op, const mx_linear_qtens
   p.tiles_j = static_cast<int>(pl.tiles_j);
   p.splits = pl.splits;
   p.split_steps = pl.split_steps;
-  const LinVariant v = variant(pl);
+  const LinVariant v = variant(pl, dtype == MX_F32);
   // out's type, and whether the products are exact
   auto multiply = [&](auto t, auto exact) {
     using T = decltype(t);
@@ -394,7 +432,7 @@ hipError_t launch_lin8_product(const LinGeom& g, LinOp op, const mx_linear_qtens
     auto launch = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(v.workgroups)), dim3(v.threads), 0, s, p); };
     auto with = [&](auto contract) {
       constexpr bool C = decltype(contract)::value;
-      pl.shape == 2 ? launch(k_lin8_product<T, Big, C, X>) : pl.shape == 1 ? launch(k_lin8_product<T, Small, C, X>) : launch(k_lin8_product<T, Tiny, C, X>);
+      pl.shape == 2 ? launch(k_lin8_product<T, Big, C, X>) : pl.shape == 1 ? launch(k_lin8_product<T, Small, C, X>) : launch(k_lin8_product<T, Tiny<X>, C, X>);
     };
     op == LIN_WGRAD ? with(std::true_type{}) : with(std::false_type{});
   };
