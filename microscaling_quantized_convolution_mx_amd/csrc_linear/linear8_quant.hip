@@ -8,7 +8,7 @@
 // together in LDS, the column form's transposed by the lanes' 8 rows, and
 // written as whole stripes.
 //
-// Bound by memory traffic: 16384x8192 bf16 76 us for the row form (5.3 TB/s, a
+// Bound by memory traffic: 16384x8192 bf16 74 us for the row form (5.4 TB/s, a
 // large copy's rate), 79 for the column form, 107 for both (5.0); dequantizing
 // the row form to bf16 64 (6.3 TB/s, most of it stores past the caches), to fp32
 // 8192x8192 94.  The column form dequantizes at 3.3 TB/s: its bytes go through
@@ -164,6 +164,38 @@ __global__ __launch_bounds__(256) void k_lin8_quantize(const Quant8Params p) {
   }
 }
 
+// The row form alone in 1x128 blocks: nothing joins the rows, so a workgroup
+// takes a stripe of 32 and a lane 2 of them.  A launch that leaves CUs idle lasts
+// as long as one lane's work, and large ones have more waves to hide memory with:
+// 33x1024 2.6 us in a HIP graph, 3.9 by whole blocks; 301x1999 fp32 3.1 and 5.8;
+// 2048x4096 bf16 5.3 and 5.7; 8192^2 bf16 30.6 and 31.2, fp32 58.5 and 61.8.
+template <class T>
+__global__ __launch_bounds__(256) void k_lin8_quantize_stripes(const Quant8Params p) {
+  __shared__ __attribute__((aligned(16))) uint8_t rtile[4096];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, q = lane & 15;
+  const uint32_t stripe = blockIdx.y, by = blockIdx.x / p.ncb, bx = blockIdx.x - by * p.ncb;
+  Rows at;
+  if (!find_rows(p, by, at)) return;
+  const int r0 = 8 * wave + 2 * g;  // of the stripe
+  const int64_t c = static_cast<int64_t>(bx) * kPad + 8 * q, first = 32 * static_cast<int64_t>(stripe) + r0;
+  Raw8<T> raw[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    raw[i] = load_raw8(static_cast<const T*>(p.src) + (at.row0 + first + i) * p.ld, c, first + i < at.left ? p.cols : 0);
+  uint8_t* scales = p.rscales + (at.prow / kPad * (p.rkt / 2) + bx) * k8ScaleBytes + stripe;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float x[8];
+    unpack8(raw[i], x);
+    const uint32_t code = block8_code(row16_max(amax8(x)));
+    *reinterpret_cast<uint2*>(rtile + piece_row(r0 + i, q / 2) + 8 * (q & 1)) = encode8x8(x, code);
+    if (q == 0) scales[(r0 + i) * 4] = static_cast<uint8_t>(code);
+  }
+  __syncthreads();
+  *reinterpret_cast<i32x4*>(p.rcodes + ((at.prow / kTileR + stripe) * p.rkt + 2 * static_cast<int64_t>(bx)) * k8TileBytes + 16 * tid) =
+      *reinterpret_cast<const i32x4*>(rtile + piece_row(tid & 31, tid >> 5));
+}
+
 // Workgroups, waves and lanes as in the quantizer, but a wave's rows in the
 // order of memory: a load takes 4 rows that share their lines.  COLS: from the
 // column form, byte by byte through LDS.  STREAM: past the caches, rows at
@@ -267,7 +299,8 @@ hipError_t launch_lin8_quantize(const LinGeom& g, mx_role role, int block, const
     constexpr bool S = decltype(square)::value;
     if (p.rcodes && p.ccodes) go(k_lin8_quantize<T, S, true, true>);
     else if (p.ccodes) go(k_lin8_quantize<T, S, false, true>);
-    else go(k_lin8_quantize<T, S, true, false>);
+    else if constexpr (S) go(k_lin8_quantize<T, true, true, false>);
+    else hipLaunchKernelGGL(k_lin8_quantize_stripes<T>, dim3(n, 4), dim3(256), 0, s, p);
   };
   auto as = [&](auto t) { block == kPad ? with(t, std::true_type{}) : with(t, std::false_type{}); };
   switch (dtype) {

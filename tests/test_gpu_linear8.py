@@ -60,6 +60,22 @@ def test_quantize_values(dt, block):
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
+def test_row_form_alone(dt):
+    """Bit for bit the row form that is written beside the column form, codes, scales and
+    padding, of one layer, of experts and of weights."""
+    for m, n, k, lens in [(1, 8, 1, None), (97, 8, 300, None), (700, 8, 1999, None), (4100, 8, 2170, None), (301, 130, 260, [0, 33, 128, 0, 131])]:
+        say("row form", dt, m, n, k, lens)
+        d = mx.linear_desc(m, n, k, experts=len(lens or ()), block=1)
+        x, off = rand(5, m, k, dt=dt, spread=5.0).to(DEV), offsets_of(lens, 4) if lens else None
+        w = rand(6, *([len(lens)] if lens else []), n, k, dt=dt, spread=5.0).to(DEV)
+        for role, t, o in ((ACT, x, off), (WEIGHT, w, None)):
+            for u in (t, strided(t.cpu(), 3, 1)):
+                one, both = quantize(d, role, u, off=o, cols=False), quantize(d, role, u, off=o)
+                for g, e in zip(one.buffers[0], both.buffers[0]):
+                    same(g.cpu().numpy(), e.cpu().numpy(), f"{m}x{k} {lens} role {role}")
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
 @pytest.mark.parametrize("form", [0, 1])
 def test_dequantize_types_and_strides(dt, form):
     m, k = 200, 300
