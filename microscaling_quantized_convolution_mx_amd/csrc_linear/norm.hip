@@ -413,21 +413,27 @@ __global__ __launch_bounds__(256) void k_norm_dweight(const BwdParams p) {
   store_row8(p.partial + static_cast<int64_t>(blockIdx.y) * p.features, c, p.features, dw);
 }
 
-// Sums the workgroups' parts of the weight's gradient: 64 columns per
-// workgroup, 16 threads each of every 16th part, joined in their order.
+// Sums the workgroups' parts of the weight's gradient: 32 columns per
+// workgroup, 32 threads each of every 32nd part, joined in their order.
 __global__ __launch_bounds__(1024) void k_norm_reduce(const float* __restrict__ partial, int parts, int features, float* __restrict__ dw) {
-  __shared__ float sum[16][64];
-  const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + l;
+  __shared__ float sum[32][32];
+  const int l = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + l;
   float s = 0.0f;
   if (c < features) {
-#pragma unroll 8
-    for (int i = q; i < parts; i += 16) s += partial[static_cast<int64_t>(i) * features + c];
+    for (int i = q; i < parts; i += 32 * 8) {
+      float v[8];  // (loaded before the first is added, the last ones too)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = partial[static_cast<int64_t>(min(i + 32 * j, parts - 1)) * features + c];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += i + 32 * j < parts ? v[j] : 0.0f;
+    }
   }
   sum[q][l] = s;
   __syncthreads();
   if (q == 0 && c < features) {
-    for (int i = 1; i < 16; ++i) s += sum[i][l];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) s += sum[i][l];
     dw[c] = s;
   }
 }
@@ -543,7 +549,7 @@ hipError_t launch_norm_bwd(const mx_norm_desc& d, const NormBwd& a, void* worksp
     });
   });
   if (a.dweight)
-    hipLaunchKernelGGL(k_norm_reduce, dim3((d.features + 63u) / 64), dim3(1024), 0, s, p.partial, d.tokens > 0 ? groups : 0, d.features, a.dweight);
+    hipLaunchKernelGGL(k_norm_reduce, dim3((d.features + 31u) / 32), dim3(1024), 0, s, p.partial, d.tokens > 0 ? groups : 0, d.features, a.dweight);
   return hipGetLastError();
 }
 
