@@ -32,8 +32,6 @@ namespace {
 // half of a SIMD's, which two workgroups share.)
 int stripes8_per_group(int64_t stripes) { return std::min(stripes_per_group(stripes), 2); }
 
-constexpr size_t kTokenLds = size_t{64} << 10;  // for a pass' tokens in bf16: two workgroups share a CU where there are that many
-
 // TX: type of the unquantized tokens, void for codes.
 template <class TX, int SN>
 __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin8_few(const FewParams p) {
@@ -138,9 +136,17 @@ size_t fused_lds(int64_t kt, int waves, int tokens) {
   return ((x > s ? x : s) + 15) / 16 * 16;
 }
 
-int tokens_per_pass(int64_t kt) {
+// Tokens of a pass, whose LDS is the most that any workgroup may need.  Without
+// experts a pass has all tokens, and two workgroups share a CU.  With experts,
+// most of which have few, as many share it as its registers hold, 16 waves, and
+// an expert with more tokens takes more passes: 64 tokens of 64 experts,
+// 2048x1024, 23.5 us evenly spread (5.7 TB/s of weight), 16.4 at random, 9.9 all on
+// one expert; with 64 KiB for every workgroup 27.4, 19.6 and 12.8 (1024x512,
+// 256 tokens at random, 9.1 and 8.9).
+int tokens_per_pass(int64_t kt, bool experts) {
+  const size_t most = experts ? std::min<size_t>(64, 10 * waves_of(kt)) << 10 : size_t{64} << 10;
   int t = 32;
-  while (t > 0 && fused_lds(kt, waves_of(kt), t) > kTokenLds) --t;
+  while (t > 0 && fused_lds(kt, waves_of(kt), t) > most) --t;
   return t;
 }
 
@@ -164,7 +170,7 @@ FewParams make_few(const LinGeom& g, bool dgrad, bool fused, const mx_linear_qte
   p.experts = g.e;
   const int64_t stripes = (p.n + kTileR - 1) / kTileR;
   sn = stripes8_per_group(stripes * g.ew);
-  const int64_t most = fused ? tokens_per_pass(p.kt) : 32;
+  const int64_t most = fused ? tokens_per_pass(p.kt, g.e > 0) : 32;
   p.per_pass = static_cast<int>(g.m < most ? g.m : most);
   // an expert with tokens has one pass, and one more for every per_pass tokens past its first
   const int64_t used = g.m < g.ew ? g.m : g.ew;
@@ -197,7 +203,7 @@ LinVariant lin8_few_variant(const LinGeom& g, bool dgrad, bool fused) {
 // the 4-bit kernel.
 bool lin8_fused(const LinGeom& g) {
   const int64_t kt = g.kp / kTileC, stripes = (g.n + kTileR - 1) / kTileR;
-  const int t = tokens_per_pass(kt), sn = stripes8_per_group(stripes * g.ew);
+  const int t = tokens_per_pass(kt, g.e > 0), sn = stripes8_per_group(stripes * g.ew);
   const int64_t groups = (stripes + sn - 1) / sn;
   if (t == 0 || g.m * g.kp * groups >= (int64_t{1} << 24)) return false;
   return g.e == 0 ? g.m <= t : lin8_few(g);

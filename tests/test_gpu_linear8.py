@@ -443,6 +443,26 @@ def test_apply_experts(lens, first, rest):
     assert np.isnan(got[:first]).all() and np.isnan(got[first + sum(lens):]).all()
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("k", [64, 520, 1100, 2050])
+def test_apply_experts_in_passes(k, dt):
+    """Experts with more tokens than a pass has, by 1, 2, 4 and 8 waves."""
+    lens = [45, 0, 1, 33, 0, 2, 19, 20] + [0] * 4
+    say("apply experts in passes", k, dt)
+    m, n, e = sum(lens), 100, len(lens)
+    off = offsets_of(lens, 0)
+    d = mx.linear_desc(m, n, k, experts=e, block=128)
+    x, w = rand(3, m, k, dt=dt), rand(4, e, n, k, dt=dt)
+    wq = quantize(d, WEIGHT, w.to(DEV), cols=False)
+    y = torch.full((m, n), float("nan"), dtype=torch.float32, device=DEV)
+    mx.mx_linear8_apply(d, wq, x.to(DEV), y, workspace(d), offsets=off)
+    got, xv = f64(y), R.form(f64(x), 1, 0)
+    for i, (a, b) in enumerate(R.segments(m, off.tolist())):
+        wv = R.form(f64(w[i]), 128, 0)
+        ref = xv[a:b] @ wv.T
+        assert np.all(np.abs(got[a:b] - ref) <= R.bound(k, xv[a:b], wv.T, ref, "f32")), (i, k)
+
+
 @pytest.mark.parametrize("m", [3, 200])
 def test_apply_non_finite(m):
     n, k = 170, 300
