@@ -16,8 +16,8 @@
 // arrives.  Tokens quantized here are kept in LDS as bf16.
 //
 // Measured in graphs of such calls, which leave the weight in the last-level
-// cache: 1x16384x8192 22.8 us (5.9 TB/s of weight) or, quantizing, 24.6,
-// 1x4096x4096 5.7 and 5.5 (128 workgroups: half of the CUs), 256 tokens of 64
+// cache: 1x16384x8192 22.8 us (5.9 TB/s of weight) or, quantizing, 23.9,
+// 1x4096x4096 5.7 and 5.2 (128 workgroups: half of the CUs), 256 tokens of 64
 // experts, 2048x2048, 42 (6.4 TB/s).
 #include <algorithm>
 #include <type_traits>
@@ -40,6 +40,8 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin8_few(const FewParams 
   // quantizing 5.4 us, 7.6 with 6 of them, 5.8 with 8 in all registers; not
   // quantizing 5.7, 7.3 with 4, which spill)
   constexpr int kAhead = SN == 1 ? kFused ? 4 : 3 : 2;
+  // loads of the tokens at once (20x4096x1024 7.4 us, 8.0 with one; 31x1024x1024 9.5 and 10.4)
+  constexpr int kLoads = sizeof(std::conditional_t<kFused, TX, float>) == 2 ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
@@ -74,15 +76,26 @@ __global__ __launch_bounds__(64 * kMaxWaves, 4) void k_lin8_few(const FewParams 
 
   if constexpr (kFused) {
     // a thread takes a token's 8 columns at a time, 16 of them a block; 8
-    // columns c/8 of token r are at (c/8 * nt + r) * 16
-    const int nc = kt * (kTileC / 8);
-    for (int b = tid; b < nc * nt; b += threads) {
-      const int r = b / nc, c = b - r * nc;
-      float v[8];
-      load_row8(static_cast<const TX*>(p.x) + (row0 + r) * p.ldx, static_cast<int64_t>(c) * 8, p.k, v);
-      const uint32_t code = block8_code(row16_max(amax8(v)));
-      const uint2 e = encode8x8(v, code);
-      reinterpret_cast<bf16x8*>(lds)[c * nt + r] = widen8(static_cast<int>(e.x), static_cast<int>(e.y), __uint_as_float(code << 23));
+    // columns c/8 of token r are at (c/8 * nt + r) * 16.  (An odd stride between
+    // columns, free of bank conflicts, changes nothing.)
+    const int nc = kt * (kTileC / 8), all = nc * nt;
+    for (int b0 = tid; b0 < all; b0 += kLoads * threads) {
+      Raw8<TX> raw[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int b = b0 + i * threads, r = b / nc, c = b - r * nc;
+        if (b < all) raw[i] = load_raw8(static_cast<const TX*>(p.x) + (row0 + r) * p.ldx, static_cast<int64_t>(c) * 8, p.k);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int b = b0 + i * threads, r = b / nc, c = b - r * nc;
+        if (b >= all) break;  // (blocks are whole: 16 lanes)
+        float v[8];
+        unpack8(raw[i], v);
+        const uint32_t code = block8_code(row16_max(amax8(v)));
+        const uint2 e = encode8x8(v, code);
+        reinterpret_cast<bf16x8*>(lds)[c * nt + r] = widen8(static_cast<int>(e.x), static_cast<int>(e.y), __uint_as_float(code << 23));
+      }
     }
     __syncthreads();
   }
