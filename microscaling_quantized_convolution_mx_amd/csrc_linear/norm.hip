@@ -13,7 +13,7 @@
 // read twice.
 //
 // Measured: 16384x4096 bf16 forward 104 us (5.1 TB/s, a large copy's rate),
-// backward 105 (5.1, the second kernel among it), 8192x8192 with the output in
+// backward 103 (5.2, the second kernel among it), 8192x8192 with the output in
 // 8 bits 103 (4.6); 16384x5000, rows that share cache lines, forward 139 (4.7), in
 // 8 bits 175 (3.3).  One row at a time fills the CUs better than several, whose
 // registers leave room for fewer waves (8192x8192 forward 101 us, 116 with 2 rows
