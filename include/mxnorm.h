@@ -11,8 +11,11 @@
  *     dx = rstd * (g - h * mean(g * h)) + dtotal      (x's and the residual's gradient alike)
  *     dweight = sum over the tokens of dy * h
  * Sums, h and g are fp32 or more, each result is rounded once.  Sums have a
- * fixed order: results are bit-reproducible.  A row whose sum of squares
- * overflows fp32 has an rstd of 0, as one with an Inf.
+ * fixed order: results are bit-reproducible.  Squares are summed in fp64, which
+ * holds those of all finite values: rows of any size are normed alike.  rstd is
+ * rounded to fp32: a subnormal of fewer bits where the root is over 2^126, and
+ * Inf, and y with it, where it is 2^-128 or less.  A row with an Inf has an rstd
+ * of 0.
  *
  * Matrices are [tokens][features] with a row stride in elements, of any
  * alignment that the type has.  total may be x or the residual, and dx may be

@@ -100,11 +100,25 @@ __device__ __forceinline__ S row_sum(S v, S (*buf)[MOST / 64], int turn) {
   return v;
 }
 
-// 1 / sqrt(x): the fp32 value and one Newton step in fp64.
+// 1 / sqrt(x): the hardware's value, good to some 23 bits, and two Newton steps.
 __device__ __forceinline__ double inverse_root(double x) {
-  const float f = 1.0f / __builtin_sqrtf(static_cast<float>(x));
-  const double r = f;
-  return f > 0.0f && f < __builtin_inff() ? r * (1.5 - 0.5 * x * r * r) : r;
+  const double r0 = __builtin_amdgcn_rsq(x);
+  double r = r0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(0.5 * r, __builtin_fma(-(x * r), r, 1.0), r);
+  return r0 > 0.0 && r0 < __builtin_inf() ? r : r0;
+}
+
+// q + x^2 of 8 elements.  fp64 has room for the square of every fp32: in fp32 the
+// squares of elements over 2^64 would be Inf, or their sum by how many a thread
+// has, and those under 2^-75 zero.
+__device__ __forceinline__ double add_squares(const float* x, double q) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double v = x[i];
+    q = __builtin_fma(v, v, q);
+  }
+  return q;
 }
 
 // t * (hi + lo) * w, of which hi + lo is rstd, rounded to fp32, inexact results to the neighbour with an
@@ -179,15 +193,14 @@ __global__ __launch_bounds__(MOST) void k_norm_fwd(const FwdParams p) {
           add_residual(v[j], r[j], sum);
         }
       }
-      float q = 0.0f;
+      double q = 0.0;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         float x[8];
         unpack8(v[j], x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q += x[i] * x[i];
+        q = add_squares(x, q);
       }
-      const double s = row_sum<WAVE, MOST>(static_cast<double>(q), buf, turn);
+      const double s = row_sum<WAVE, MOST>(q, buf, turn);
       const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
       const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
       if (p.a.rstd && t == 0 && in) p.a.rstd[row] = hi;
@@ -249,14 +262,11 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
     double s = 0.0;
     if (row < p.tokens) {
-      float q = 0.0f;
       for (int64_t c = 8 * threadIdx.x; c < p.features; c += 8 * TPR) {
         float v[8];
         load_total<T>(p, row, c, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q += v[i] * v[i];
+        s = add_squares(v, s);
       }
-      s = q;
     }
     s = row_sum<false, TPR>(s, buf, turn);
     const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
