@@ -47,7 +47,9 @@ typedef struct {
  *   y         NULL: not stored
  *   yq        NULL, or a tensor whose row form takes y in 8 bits, the
  *             activation of mx_linear8_fwd on a layer without experts (E4M3,
- *             1x128 blocks, rounded from y's fp32; its column form is ignored)
+ *             1x128 blocks; its column form is ignored).  Its codes are those of
+ *             total * rstd * weight with rstd in fp64, rounded once; quantizing a
+ *             stored y, which has been rounded, may give others next to ties
  *   rstd      NULL, or fp32 [tokens], for the gradients
  * One of total, y, yq and rstd is needed. */
 mx_status mx_norm_fwd(const mx_norm_desc* desc, const void* x, int64_t ldx, const void* residual, int64_t ldr, mx_dtype dtype,

@@ -121,19 +121,24 @@ __device__ __forceinline__ double add_squares(const float* x, double q) {
   return q;
 }
 
-// t * (hi + lo) * w, of which hi + lo is rstd, rounded to fp32, inexact results to the neighbour with an
-// odd last bit, so that rounding the result again, to E4M3, gives what rounding
-// the product once would: codes are off only where rstd's own error, some
-// 10^-9, reaches a tie.
-__device__ __forceinline__ float odd_product(float t, float hi, float lo, float w) {
-  const float h = t * hi, e = __builtin_fmaf(t, lo, __builtin_fmaf(t, hi, -h));
-  const float y = h * w;
-  const float d = __builtin_fmaf(h, w, -y) + e * w;  // what the product has more than y
-  // towards zero where the signs differ (d is 0 where y is), and then odd; an
-  // overflow stays as it is, d being Inf then
-  const int b = __float_as_int(y), odd = (b + ((__float_as_int(d) ^ b) >> 31)) | 1;
-  constexpr int kFinite = 0x198;  // a normal or subnormal number of either sign
-  return __int_as_float(__builtin_amdgcn_classf(d, kFinite) ? odd : b);
+// y rounded to fp32, inexact values to the neighbour with an odd last bit: of the
+// 24 bits the last then says whether there was more, so that rounding the result
+// again, to E4M3's 4, gives what rounding y once would.
+__device__ __forceinline__ float round_odd(double y) {
+  const float f = static_cast<float>(y);
+  const double d = y - static_cast<double>(f);  // what y has more than f, exactly
+  // towards zero where the signs differ (f has y's), and then odd; an overflow stays as
+  // it is, d being infinite then
+  const int b = __float_as_int(f), up = static_cast<int>(__builtin_bit_cast(uint64_t, d) >> 32);
+  constexpr int kFinite = 0x198;  // a normal or subnormal number of either sign, not zero
+  return __int_as_float(__builtin_amdgcn_class(d, kFinite) ? (b + ((up ^ b) >> 31)) | 1 : b);
+}
+
+// What goes to 8 bits: t rstd w with rstd in fp64.  t w is exact there, the rest is
+// off by (32 + features / 1024) 2^-53 at most: codes differ from those of the exact
+// product only where it is nearer to a tie than that.
+__device__ __forceinline__ float code_value(float t, double r, float w) {
+  return round_odd(static_cast<double>(t) * static_cast<double>(w) * r);
 }
 
 __device__ __forceinline__ int64_t code_place(const FwdParams& p, int64_t row, int64_t c) {
@@ -202,7 +207,7 @@ __global__ __launch_bounds__(MOST) void k_norm_fwd(const FwdParams p) {
       }
       const double s = row_sum<WAVE, MOST>(q, buf, turn);
       const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
-      const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
+      const float hi = static_cast<float>(r);
       if (p.a.rstd && t == 0 && in) p.a.rstd[row] = hi;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
@@ -221,7 +226,11 @@ __global__ __launch_bounds__(MOST) void k_norm_fwd(const FwdParams p) {
           if (c < 8 * p.chunks) {
             // (a row's padded columns are zeros of x and the weight; where rstd is not finite they share a block of NaNs)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = in ? odd_product(x[i], hi, lo, w[j][i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+              // (the empty asm keeps the row and the weight in fp32 until here: in fp64 they would take twice the registers)
+              asm("" : "+v"(x[i]), "+v"(w[j][i]));
+              y[i] = in ? code_value(x[i], r, w[j][i]) : 0.0f;
+            }
             const uint2 e = encode_codes(p, row, c, y);
             if constexpr (GROUP == 1) *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = e;
             else *reinterpret_cast<uint2*>(stage + (wave * CH + j) * 512 * GROUP + ((lane / 2) * GROUP + b) * 16 + 8 * (lane % 2)) = e;
@@ -270,7 +279,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
     }
     s = row_sum<false, TPR>(s, buf, turn);
     const double r = inverse_root(s / p.features + static_cast<double>(p.eps));
-    const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
+    const float hi = static_cast<float>(r);
     if (p.a.rstd && threadIdx.x == 0 && row < p.tokens) p.a.rstd[row] = hi;
     for (int64_t c = 8 * threadIdx.x; c < 8 * static_cast<int64_t>(p.chunks); c += 8 * TPR) {
       float v[8] = {}, w[8] = {}, y[8];
@@ -287,7 +296,7 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_long(const FwdParams p) {
       }
       if constexpr (CODES) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = in && c + i < p.features ? odd_product(v[i], hi, lo, w[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) y[i] = in && c + i < p.features ? code_value(v[i], r, w[i]) : 0.0f;
         *reinterpret_cast<uint2*>(p.a.codes + code_place(p, row, c) + c % 16) = encode_codes(p, row, c, y);
       }
     }
