@@ -2,8 +2,9 @@
 
 The functions have the names of the C entry points and marshal arguments
 only; see the header for what each computes.  expert is int32 and weight
-float32, contiguous [tokens, choices]; tokens' matrices are [tokens, features],
-rows' matrices [tokens * choices, features], as in linear.py.
+float32, contiguous [tokens, choices], the tokens over any leading dimensions,
+or flattened; tokens' matrices are [tokens, features], rows' matrices [tokens *
+choices, features], as in linear.py.
 
 A layer of experts, each token's weights and experts from its router:
 
@@ -64,8 +65,8 @@ def route_desc(tokens: int, choices: int, experts: int, features: int) -> mx_rou
     return mx_route_desc(tokens, choices, experts, features)
 
 
-def _array(t, n: int, dtype, what: str):
-    """(address, device) of n contiguous elements of a type."""
+def _array(t, n: int, dtype, what: str, choices: int = 1):
+    """(address, device) of n contiguous elements of a type, `choices` of each token."""
     if t is None:
         return None, None
     if not isinstance(t, _l._torch.Tensor):
@@ -74,6 +75,9 @@ def _array(t, n: int, dtype, what: str):
         raise ValueError(f"{what}: must be a contiguous {str(dtype)[6:]} tensor, got {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{what}: {t.numel()} values, the call needs {n}")
+    # (tokens may have any leading dimensions, or all be flattened; a [choices, tokens] tensor is not meant)
+    if 1 < choices < n and t.dim() > 1 and t.shape[-1] != choices:
+        raise ValueError(f"{what}: must be [{n // choices}, {choices}], got {tuple(t.shape)}")
     at = t.get_device()
     if at < 0:
         _l._in_host_memory(t, what)
@@ -96,9 +100,9 @@ def mx_route_workspace_bytes(d: mx_route_desc) -> int:
 def mx_route_sort(d: mx_route_desc, expert, offsets, rows, order=None, workspace=None, stream=None) -> None:
     L = _load()
     n, i32 = d.tokens * d.choices, _l._torch.int32
-    e, eat = _array(expert, n, i32, "expert")
+    e, eat = _array(expert, n, i32, "expert", d.choices)
     o, oat = _array(offsets, d.experts + 1, i32, "offsets")
-    r, rat = _array(rows, n, i32, "rows")
+    r, rat = _array(rows, n, i32, "rows", d.choices)
     q, qat = _array(order, n, i32, "order")
     ws, nb, wat = _l._bytes(workspace, "workspace")
     _l._check(L.mx_route_sort(d, e, o, r, q, ws, nb, _mx._stream(stream, eat, oat, rat, qat, wat)), "mx_route_sort")
@@ -108,7 +112,7 @@ def mx_route_gather(d: mx_route_desc, x, rows, out, stream=None) -> None:
     """out[rows[t][j]] = x[t]."""
     L = _load()
     px, ldx, xat, po, ldo, oat, dt = _pair(d, x, out, "x", "out")
-    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows")
+    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows", d.choices)
     _l._check(L.mx_route_gather(d, px, ldx, r, po, ldo, dt, _mx._stream(stream, xat, oat, rat)), "mx_route_gather")
 
 
@@ -116,7 +120,7 @@ def mx_route_gather_bwd(d: mx_route_desc, dout, rows, dx, stream=None) -> None:
     """dx[t] = sum over j of dout[rows[t][j]]."""
     L = _load()
     px, ldx, xat, po, ldo, oat, dt = _pair(d, dx, dout, "dx", "dout")
-    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows")
+    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows", d.choices)
     _l._check(L.mx_route_gather_bwd(d, po, ldo, r, px, ldx, dt, _mx._stream(stream, xat, oat, rat)), "mx_route_gather_bwd")
 
 
@@ -124,8 +128,8 @@ def mx_route_combine(d: mx_route_desc, y, rows, weight, out, stream=None) -> Non
     """out[t] = sum over j of weight[t][j] * y[rows[t][j]]."""
     L = _load()
     po, ldo, oat, py, ldy, yat, dt = _pair(d, out, y, "out", "y")
-    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows")
-    w, wat = _array(weight, d.tokens * d.choices, _l._torch.float32, "weight")
+    r, rat = _array(rows, d.tokens * d.choices, _l._torch.int32, "rows", d.choices)
+    w, wat = _array(weight, d.tokens * d.choices, _l._torch.float32, "weight", d.choices)
     _l._check(L.mx_route_combine(d, py, ldy, r, w, po, ldo, dt, _mx._stream(stream, oat, yat, rat, wat)), "mx_route_combine")
 
 
@@ -137,8 +141,8 @@ def mx_route_combine_bwd(d: mx_route_desc, dout, y, rows, weight, dy=None, dweig
     if dy is not None and ddt != dt:
         raise ValueError(f"dy: must have dout's type, got {dy.dtype}")
     n = d.tokens * d.choices
-    r, rat = _array(rows, n, _l._torch.int32, "rows")
-    w, wat = _array(weight, n, _l._torch.float32, "weight")
-    g, gat = _array(dweight, n, _l._torch.float32, "dweight")
+    r, rat = _array(rows, n, _l._torch.int32, "rows", d.choices)
+    w, wat = _array(weight, n, _l._torch.float32, "weight", d.choices)
+    g, gat = _array(dweight, n, _l._torch.float32, "dweight", d.choices)
     _l._check(L.mx_route_combine_bwd(d, po, ldo, py, ldy, r, w, pd, ldd, g, dt,
                                      _mx._stream(stream, oat, yat, dat, rat, wat, gat)), "mx_route_combine_bwd")

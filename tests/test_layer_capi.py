@@ -245,3 +245,36 @@ def test_tensors_on_the_streams_device_pass(reached, call):
         (name, got), = reached
         assert name == "mx_" + call and got == handle
         reached.clear()
+
+
+@pytest.mark.parametrize("call,arg", [("route_sort", "expert"), ("route_sort", "rows"), ("route_gather", "rows"), ("route_gather_bwd", "rows"),
+                                      ("route_combine", "rows"), ("route_combine", "weight"), ("route_combine_bwd", "rows"),
+                                      ("route_combine_bwd", "weight"), ("route_combine_bwd", "dweight")])
+def test_choices_by_tokens_instead_of_tokens_by_choices(reached, call, arg):
+    """[choices, tokens] has as many values, which would be taken for other tokens' choices."""
+    m, c, k = 10, 2, 100
+    r = mx.route_desc(m, c, 4, k)
+    dev = on(0)
+
+    def arrays(swap):
+        def a(name, dtype):
+            shape = swap(name)
+            return torch.zeros(*shape, dtype=dtype).as_subclass(dev)
+        i32, f32 = torch.int32, torch.float32
+        rows, weight = (lambda: a("rows", i32)), (lambda: a("weight", f32))
+        x, xs = (torch.zeros(n, k).as_subclass(dev) for n in (m, m * c))
+        off = torch.zeros(5, dtype=i32).as_subclass(dev)
+        {"route_sort": lambda: mx.mx_route_sort(r, a("expert", i32), off, rows()),
+         "route_gather": lambda: mx.mx_route_gather(r, x, rows(), xs),
+         "route_gather_bwd": lambda: mx.mx_route_gather_bwd(r, xs, rows(), x),
+         "route_combine": lambda: mx.mx_route_combine(r, xs, rows(), weight(), x),
+         "route_combine_bwd": lambda: mx.mx_route_combine_bwd(r, x, xs, rows(), weight(), None, a("dweight", f32))}[call]()
+    with pytest.raises(ValueError, match=rf"{arg}: must be \[10, 2\]"):
+        arrays(lambda name: (c, m) if name == arg else (m, c))
+    assert not reached
+    for shape in ((m, c), (m * c,), (5, 2, c)):
+        arrays(lambda name: shape)
+    assert len(reached) == 3
+    # one choice, or one token, reads alike
+    for r, shape in ((mx.route_desc(m * c, 1, 4, k), (5, 4)), (mx.route_desc(1, m * c, 4, k), (m * c, 1))):
+        MR._array(torch.zeros(shape, dtype=torch.int32).as_subclass(dev), m * c, torch.int32, "rows", r.choices)
