@@ -290,3 +290,11 @@ def test_matrices_past_32_bits():
     h = c * rstd.double()[:, None]
     ref, lim = f64((c * h).sum(0)), (m + 3) * R.U * 1.01 * f64((c * h).abs().sum(0))
     assert np.all(np.abs(f64(dw[at]) - ref) <= lim)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("k", [300, 1100, 5000, 9000])
+def test_forward_many_rows_in_other_types(k, dt):
+    """The kernels that write four rows' codes together, from 1024 rows on, with a residual and every other output."""
+    say("forward", k, dt)
+    forward_case(1030, k, dt, dt, "f32")
