@@ -143,3 +143,76 @@ def test_a_step_in_a_graph(example):
 def test_example_runs(example):
     losses, off = example.main(steps=4)
     assert len(losses) == 4 and all(math.isfinite(v) for v in losses) and math.isfinite(off)
+
+
+@pytest.mark.parametrize("tokens", [1, 37, 700])
+def test_router_gradient(example, tokens):
+    """The router's gradient and its part of the tokens', which the example adds up itself: against the formula in 64 bits, and
+    against differences of the loss."""
+    E, C, F = example.EXPERTS, example.CHOICES, example.FEATURES
+    layer = example.Layer(tokens, 14)
+    g = torch.Generator(device=DEV).manual_seed(15)
+    x, dout = (torch.randn(tokens, F, device=DEV, generator=g).bfloat16() for _ in range(2))
+    layer.norm.copy_(torch.linspace(0.5, 1.5, F))
+    layer.forward(x)
+    layer.backward(dout)
+    w, dw, h, router = f64(layer.weight), f64(layer.dweight), f64(layer.h), f64(layer.router)
+    expert, rows = layer.expert.cpu().numpy(), layer.rows.long()
+    inner = (w * dw).sum(1, keepdims=True)
+    # C products and their sum, a difference and a product: C + 3 roundings, none of a larger value than this
+    d, d_err = w * (dw - inner), (C + 3) * RN.U * 1.01 * w * (np.abs(dw) + np.abs(w * dw).sum(1, keepdims=True))
+    logits, err = np.zeros((tokens, E)), np.zeros((tokens, E))
+    np.put_along_axis(logits, expert, d, 1)
+    np.put_along_axis(err, expert, d_err, 1)
+    ref = logits.T @ h
+    within(layer.drouter, ref, err.T @ np.abs(h) + (tokens + 2) * RN.U * 1.01 * (np.abs(logits) + err).T @ np.abs(h))
+    # its part of dh is rounded to bf16, and so is the sum with the rows' part
+    alone = torch.empty_like(layer.dh)
+    mx.mx_route_gather_bwd(layer.rd, layer.dhs, layer.rows, alone)
+    part = logits @ router
+    lim = err @ np.abs(router) + (E + 2) * RN.U * 1.01 * (np.abs(logits) + err) @ np.abs(router)
+    lim = RN.bound(part, lim, "bf16")
+    within(layer.dh, f64(alone) + part, RN.bound(f64(alone) + part, lim, "bf16"))
+
+    # <dout, out> over the routers with the same choices and rows of the experts.  A weight's third derivative by a logit is at most
+    # 1/8, so a step of 2^-10 in an element of size h moves the quotient by 2^-20 / 6 * h^3 / 8 of the terms, and 64-bit rounding by 2^-52 / 2^-10
+    ys = f64(layer.ys)
+    parts = np.stack([f64(dout) * ys[rows[:, j].cpu().numpy()] for j in range(C)], 1)
+    terms, mags = parts.sum(2), np.abs(parts).sum(2).max(1)
+
+    def loss(r):
+        z = np.take_along_axis(h @ r.T, expert, 1)
+        p = np.exp(z - z.max(1, keepdims=True))
+        return float((p / p.sum(1, keepdims=True) * terms).sum())
+    step = 2.0 ** -10
+    for e, c in ((0, 0), (3, 200), (int(expert[0, 0]), 17), (int(expert[-1, 1]), F - 1)):
+        a, b = router.copy(), router.copy()
+        a[e, c] += step
+        b[e, c] -= step
+        got, diff = f64(layer.drouter)[e, c], (loss(a) - loss(b)) / (2 * step)
+        slack = (np.abs(h[:, c]) ** 3 * 2.0 ** -23 * np.abs(terms).sum(1)).sum() + 2.0 ** -40 * np.abs(terms).sum()
+        # dweight and the weights come in fp32: F products and their sum; a matrix product of F for the logits, each of which moves
+        # a weight by at most a quarter of its error, an exponential, a sum and a quotient
+        z_err = (F + 2) * RN.U * (np.abs(h) @ np.abs(router).T).max(1)
+        slack += ((np.abs(terms).sum(1) * (z_err + 8 * RN.U) + (F + 2) * RN.U * mags) * 2 * np.abs(h[:, c])).sum()
+        slack += (err.T @ np.abs(h) + (tokens + 2) * RN.U * np.abs(logits).T @ np.abs(h))[e, c] * 1.01
+        assert abs(got - diff) <= slack
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_serving_adds_the_products_up(example, tokens):
+    """What is served is the weighted sum of its products."""
+    C = example.CHOICES
+    layer = example.Layer(tokens, 17)
+    x = torch.randn(tokens, example.FEATURES, device=DEV, generator=torch.Generator(device=DEV).manual_seed(18)).bfloat16()
+    layer.ys.fill_(float("nan"))
+    served = layer.serve(x)
+    rows, ys, wt = layer.rows.cpu().numpy(), f64(layer.ys), f64(layer.weight)
+    out = sum(ys[rows[:, j]] * wt[:, j, None] for j in range(C))
+    mags = sum(np.abs(ys[rows[:, j]] * wt[:, j, None]) for j in range(C))
+    within(served, out, RN.bound(out, (C + 1) * RN.U * 1.01 * mags, "bf16"))
+    # through the norm, the places and the rows that the training pass has
+    h, _ = RN.norm(f64(x), f64(layer.norm), float(np.float32(1e-6)))
+    within(layer.h, h, RN.bound(h, np.abs(h) * RN.y_error(example.FEATURES), "bf16"))
+    for j in range(C):
+        same(f64(layer.hs)[rows[:, j]], f64(layer.h))
