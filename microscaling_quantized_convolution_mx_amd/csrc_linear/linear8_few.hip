@@ -17,8 +17,8 @@
 //
 // Measured in graphs of such calls, which leave the weight in the last-level
 // cache: 1x16384x8192 22.8 us (5.9 TB/s of weight) or, quantizing, 23.9,
-// 1x4096x4096 5.7 and 5.2 (128 workgroups: half of the CUs), 256 tokens of 64
-// experts, 2048x2048, 42 (6.4 TB/s).
+// 1x4096x4096 5.7 and 5.4 (128 workgroups: half of the CUs have none, which stripes of
+// 16 lines would change; not tried), 256 tokens of 64 experts, 2048x2048, 42 (6.4 TB/s).
 #include <algorithm>
 #include <type_traits>
 

@@ -23,19 +23,22 @@
 // several slices of 64 columns ahead, and from there to the registers that the
 // MFMA reads, one slice ahead.
 //
-// Measured (bf16 outputs): 8192x8192x8192 370 to 400 us, 2.8 to 3.0 PFLOP/s;
-// 16384x4096x4096 forward 201, weight gradient 181; 4096^3 54.  Exact: 735 us, 1.5
-// PFLOP/s; 388 and 362; 103.  In the 16384x4096x4096 forward the MFMA is busy 63%
-// of the time at 1.95 GHz of 2.4, in its weight gradient 74% at 1.86: power sets
-// the clock.  Neither another order of reads and copies between the MFMAs nor
-// more stages or slices between barriers changed these, the small tiles' times
-// neither (301x2500x1999 8.4 to 8.9, 2048^3 13.6 to 14.1): their copies arrive at
-// some 60 bytes per ns and CU, half of what L2's width allows.  Four rounds of 256 tiles
-// cost about 9 us each for the first operands and the stores; overlapping these
-// with the tile before has not been measured.  Experts' products take 128x128 tiles
-// at the full clock, 33% busy, bound by L2: 16 experts of 2048x2048 with 16384 uneven
-// tokens 75 us forward, and 137 for their exact weight gradients, whose stores
-// alone take 52.
+// Measured in graphs of the same call (bf16 outputs): 8192x8192x8192 373 to 389 us, 2.8 to
+// 3.0 PFLOP/s, 434 with operands that are not in the caches after a pause; 16384x4096x4096
+// forward 202, weight gradient 186; 4096^3 55.  Exact: 745 us, 1.5 PFLOP/s; 391 and 367;
+// 103.  In the 16384x4096x4096 forward the MFMA is busy 64% of the time at 1.94 GHz
+// of 2.4, in its weight gradient 75% at 1.84: power sets the clock.  Neither
+// another order of reads and copies between the MFMAs nor more stages or slices
+// between barriers changed these, the small tiles' times neither (301x2500x1999 7.0
+// to 7.6, 2048^3 11.6): their copies arrive at some 60 bytes per ns and CU,
+// half of what L2's width allows, and what limits them is not known.  Four rounds of
+// 256 tiles cost about 9 us each for the first operands and the stores; overlapping
+// these with the tile before has not been measured.  Experts' products take 128x128
+// tiles at the full clock, the MFMA busy a third of the time, since a slice's 16
+// KiB of operands take longer to arrive, at that same rate, than its products to be
+// made: 16 experts of 2048x2048 with 16384 uneven tokens 80 us forward (72 with even
+// ones), and 141 (132) for their exact weight gradients, whose stores alone
+// take 52.
 #include "linear8_codes.h"
 #include "linear_product.h"
 
@@ -54,8 +57,13 @@ struct Teams : Shape<M, N, A, B, S> {
 };
 using Big = Teams<256, 256, 2, 2, 4, 1>;
 using Small = Teams<128, 128, 2, 2, 4, 1>;
-// (two teams of exact products, whose steps are twice as long: 301x2500x1999 10.9
-// us, 12.2 with one; other products 8.6 and 8.4, 512x4096x4096 19.3 and 18.0)
+// (Two teams for exact products, whose steps take twice as long.  One against two, us,
+// whole contractions: 64x8192x8192 32.1 and 25.3, 128x2048x2048 10.8 and 9.1, 128x4096x4096
+// 19.2 and 14.8, 301x2500x1999 11.5 and 10.1, 256x1024x4096 18.5 and 14.1, 512x2048x2048 11.9 and 10.1,
+// 1024x512x2048 11.0 and 9.5, 512x1024x1024 7.6 and 7.1, 1024x1024x1024 8.0 and 7.6; even or up to 6%
+// slower where contractions are short and tiles many: 512x512x512 5.5 and 5.6, 2048x512x512 6.05 and
+// 6.1, 1024x2048x2048 15.5 and 15.8, 512x4096x1024 10.6 and 11.2.  Other products 301x2500x1999 8.4 and 8.6,
+// 512x4096x4096 18.0 and 19.3.)
 template <bool EXACT>
 using Tiny = Teams<64, 64, 2, 2, 4, EXACT ? 2 : 1>;
 
@@ -318,13 +326,17 @@ LinVariant variant(const Plan& pl, bool exact) {
 //          and round, bound by the MFMA (4096^3 54, Small 63, Tiny 99; exact 104,
 //          114, 149; the weight gradients of 16 experts' 1024 tokens, 2048x2048,
 //          exact 144, Small 131)
-//   Small  5, and 0.5 per step and round, bound by L2 (2048^3 13.4, Tiny 19, Big 26)
+//   Small  5, and 0.5 per step and round, what its operands take to arrive (2048^3
+//          13.4, Tiny 19, Big 26)
 //   Tiny   3.6, and 0.24 per step and round, bound by the latency of a step
 //          (301x2500x1999 8.5, Small 12; 512x4096x4096 17.4, Small 18.3)
 // Splitting the contraction costs a launch, 3, and the traffic of its partial
-// sums at 4 TB/s: it pays for long contractions with few outputs (256x1024x4096
-// exact 14 in 4 pieces, 19 whole; without exact products 11.6 either way).  Tiles
-// too small for a launch's 2^32 - 1 threads are left out, as in 4 bits.
+// sums at 4 TB/s: it pays for long contractions with few outputs (256x1024x4096 exact
+// 11.9 in 4 pieces, 14.1 whole, 256x512x4096 without exact products 9.2 and 10.6;
+// 64x8192x8192 in 2 pieces 20.4 and 25.3, 17.4 and 21.7).  Exact products' steps in two teams are
+// shorter than this takes them for, so that some are in more pieces than would be
+// fastest: 128x2048x2048 in 4 10.5, whole 9.1; 256x512x4096 in 8 11.3, in 4 10.5.
+// Tiles too small for a launch's 2^32 - 1 threads are left out, as in 4 bits.
 Plan make_plan(const LinGeom& g, LinOp op, bool exact) {
   const int64_t rows = op == LIN_WGRAD ? g.n : g.m, cols = op == LIN_FWD ? g.n : g.k;
   const int64_t contract = op == LIN_FWD ? g.kp : op == LIN_DGRAD ? g.np : g.mp;

@@ -10,14 +10,15 @@
 // Workgroups take rows in turn and keep the weight, and in the backward pass
 // the weight's gradient over their rows, in registers; those partial sums are
 // added by a second kernel in a fixed order.  Rows too long for registers are
-// read twice.
+// read twice (4096x20480 bf16 forward 148 us, backward 272; 4096x16384 102 and 118).
 //
-// Measured: 16384x4096 bf16 forward 104 us (5.1 TB/s, a large copy's rate),
-// backward 103 (5.2, the second kernel among it), 8192x8192 with the output in
-// 8 bits 103 (4.6); 16384x5000, rows that share cache lines, forward 139 (4.7), in
-// 8 bits 175 (3.3).  One row at a time fills the CUs better than several, whose
-// registers leave room for fewer waves (8192x8192 forward 101 us, 116 with 2 rows
-// at a time, 122 with 4).
+// Measured: 16384x4096 bf16 forward 103 us (5.2 TB/s, a large copy's rate), to 8 bits
+// 98 (4.8), backward 104 (5.2, the second kernel among it); 16384x5000, rows that share
+// cache lines, forward 137 (4.8), to 8 bits 176 (3.3; why is open).  One row at a time
+// fills the CUs better than several, whose registers leave room for fewer waves
+// (8192x8192 forward 101 us, 116 with 2 rows at a time, 122 with 4).  So does keeping
+// the row and the weight in fp32 between the arithmetic in fp64 (to 8 bits 98 us, 116
+// with both in fp64 registers; 16384x5000 176 and 248).
 #include <algorithm>
 #include <type_traits>
 

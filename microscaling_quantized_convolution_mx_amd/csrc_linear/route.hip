@@ -10,13 +10,14 @@
 // choices, without atomics.  Few choices are one workgroup's; for more, a first
 // kernel leaves each workgroup's counts and the second adds up those before it.
 //
-// 16384 tokens' 4 choices of 64 experts take 10 us, 32 tokens' 2 choices 3.5.
+// 16384 tokens' 4 choices of 64 experts take 9 to 10 us, 32 tokens' 2 choices 3 to 4.
 //
 // Moves.  Bound by memory traffic: a token's row is read, or written, once for
 // all of its choices, and each of their rows once.  A token is some lanes' of a
 // workgroup, 16 bytes each at a time.  16384 tokens of 4 choices, 2048 bf16
-// features: gather and its gradient 67 us (5.0 TB/s), combine 67, its gradient
-// 118 (5.1).  (A wave for each token: combine 84, its gradient 131.)
+// features, each repeated in a graph: gather 64 us (5.3 TB/s), its gradient 62, combine
+// 62, its gradient 115 (5.2); one after the other, on what the caches hold of the call
+// before, 52, 75, 89 and 104.  (A wave for each token: combine 84, its gradient 131.)
 #include <algorithm>
 #include <type_traits>
 
